@@ -63,8 +63,12 @@ typedef enum tgemm_status {
                               TGEMM_OUT_F32, TGEMM_OUT_BF16, or the input kind
                               of a quantizer call not TGEMM_IN_F32,
                               TGEMM_IN_BF16                                   */
-    TGEMM_ERR_SCRATCH = -8 /* ternary_gemm_s8_dx_noalloc: the split needs more
+    TGEMM_ERR_SCRATCH = -8, /* ternary_gemm_s8_dx_noalloc: the split needs more
                               than TGEMM_STATIC_SCRATCH_BYTES of scratch      */
+    TGEMM_ERR_VALUE = -9,  /* a scalar argument (eps, max_norm, act) is out of
+                              its range                                       */
+    TGEMM_ERR_WORKSPACE = -10 /* a required workspace is NULL, too small or not
+                              16-byte aligned                                 */
 } tgemm_status;
 
 /* Longest contraction for which every int32 result is exact whatever the
@@ -250,6 +254,125 @@ int ternary_quantize_rows(const void *X, int in_kind, int8_t *Q, float *scale, i
                           hipStream_t stream);
 int ternary_quantize_cols(const void *X, int in_kind, int8_t *Q, float *scale, int64_t R, int64_t C,
                           hipStream_t stream);
+
+/*
+ * The operators around the product, for a block of a network whose linear
+ * layers are ternary products: the norm that makes a product's int8 rows, the
+ * product with its bias, activation and residual addition in one pass, their
+ * backward passes, and the clipping of all gradients by their global norm.
+ * In all of them
+ *   - matrices are dense and row-major, their elements float32 or bfloat16
+ *     bit patterns by the call's kind (TGEMM_IN_*, TGEMM_OUT_*), any width,
+ *     any alignment from the element's own;
+ *   - sums and statistics are float32 (the global norm's double), summed in
+ *     a fixed order without atomics: repeated calls give identical bits;
+ *   - int8 rows and their scales are what ternary_quantize_rows would make of
+ *     the float32 values before they are rounded to the kind: s = max|y| / 127,
+ *     q = clamp(rint(y / s), -127, 127), q = 0 where s is 0 or not finite.  A
+ *     row that holds an infinity or a NaN has it as its scale;
+ *   - a call that needs a workspace takes caller-owned DEVICE memory, 16-byte
+ *     aligned, of at least the bytes that the query beside it gives
+ *     (TGEMM_ERR_WORKSPACE otherwise).  Its contents on entry do not matter;
+ *     it is in use until the call completes on `stream`;
+ *   - outputs overlap neither inputs nor each other nor the workspace
+ *     (TGEMM_ERR_ALIAS), but for the in-place forms named below, where the
+ *     two pointers are equal.
+ */
+
+/*
+ * Root-mean-square norm with the residual's addition, into int8 rows:
+ *     h = x + residual       rounded to the kind (h = x without a residual)
+ *     rstd = 1 / sqrt(sum_c h^2 / C + eps)
+ *     y = (h * rstd) * gain[c]
+ * and Q, scale from y as above.
+ *   X         [R][C] of in_kind
+ *   residual  [R][C] of in_kind, or NULL
+ *   gain      float [C]
+ *   H         [R][C] of in_kind, the sum that the residual stream goes on
+ *             with; needed with a residual (may be X or residual itself),
+ *             NULL without
+ *   Y         [R][C] of in_kind, y rounded to the kind, or NULL
+ *   rstd      float [R], or NULL (the backward pass takes it)
+ *   Q, scale  int8 [R][C], float [R]
+ * Requires R, C >= 1 (TGEMM_ERR_DIM), a finite eps >= 0 (TGEMM_ERR_VALUE).
+ * With eps = 0 a row of zeros has rstd = inf and y = NaN, as the formula does.
+ */
+int ternary_rmsnorm_quantize(const void *X, int in_kind, const void *residual, const float *gain, float eps,
+                             void *H, void *Y, float *rstd, int8_t *Q, float *scale, int64_t R, int64_t C,
+                             hipStream_t stream);
+
+/*
+ * Its backward pass, from the gradient of y (straight through the rounding
+ * to int8) and, with a residual stream, the gradient dH that reaches h past
+ * the norm.  With xhat = h * rstd and t = dy * gain,
+ *     dX[r][c]  = rstd (t - xhat * sum_c(t xhat) / C) + dH[r][c]
+ *     dgain[c]  = sum_r dy * xhat
+ * dX is the gradient of x and of the residual alike.
+ *   dY, H, dX  [R][C] of in_kind; rstd float [R]; gain float [C]
+ *   dH         [R][C] of in_kind, or NULL; dX may be dH itself
+ *   dgain      float [C] (written)
+ */
+int ternary_rmsnorm_backward(const void *dY, const void *H, int in_kind, const float *gain, const float *rstd,
+                             const void *dH, void *dX, float *dgain, int64_t R, int64_t C, void *workspace,
+                             int64_t workspace_bytes, hipStream_t stream);
+int ternary_rmsnorm_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
+
+/*
+ * Forward product with its epilogue, fused into the kernels' stores:
+ *     z = (float(acc) * a_row_scale[m]) * w_scale + bias[n]
+ *     Y[m][n] = act(z) + residual[m][n]
+ * in float32 (acc the exact int32 product), each stored matrix rounded once.
+ *   bias      float [N], or NULL
+ *   act       TGEMM_ACT_*: relu2 is max(z, 0)^2, silu z sigmoid(z), gelu_tanh
+ *             0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)))
+ *   residual  [M][N] of out_kind, or NULL; may be Y itself
+ *   Y         [M][N] of out_kind
+ *   Z         [M][N] of out_kind, z for the backward pass, or NULL
+ * The checks of ternary_gemm_s8_scaled, and TGEMM_ERR_VALUE for another act.
+ */
+#define TGEMM_ACT_NONE 0
+#define TGEMM_ACT_RELU 1
+#define TGEMM_ACT_RELU2 2
+#define TGEMM_ACT_SILU 3
+#define TGEMM_ACT_GELU_TANH 4
+int ternary_gemm_s8_epilogue(const int8_t *A, const uint8_t *Wpacked, const float *a_row_scale, float w_scale,
+                             const float *bias, int act, const void *residual, void *Y, void *Z, int out_kind,
+                             int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/*
+ * The epilogue's backward pass: from Y's gradient (which is the residual's
+ * too), in one pass over dY and Z,
+ *     dZ = dY * act'(Z)        rounded to the kind: ternary_quantize_cols and
+ *                              ternary_gemm_s8_dw take it on to dW
+ *     dbias[c] = sum_r dZ      of the unrounded values
+ *     Q, scale                 the int8 rows of the unrounded dZ: the dC of
+ *                              the dX calls
+ * relu's slope at 0 is 0.
+ *   dY, Z, dZ  [R][C] of in_kind; dbias float [C], or NULL (then no workspace
+ *   is needed); Q int8 [R][C], scale float [R]
+ */
+int ternary_epilogue_backward(const void *dY, const void *Z, int in_kind, int act, void *dZ, float *dbias,
+                              int8_t *Q, float *scale, int64_t R, int64_t C, void *workspace,
+                              int64_t workspace_bytes, hipStream_t stream);
+int ternary_epilogue_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
+
+/*
+ * Clipping of `count` gradients by their global norm:
+ *     norm = sqrt(sum over all elements of g^2)      (the sum in double)
+ *     out = g * min(1, max_norm / (norm + eps))
+ * The four arrays are HOST arrays, read before the call returns; the pointers
+ * in them are DEVICE pointers.  Gradient i has sizes[i] >= 0 elements
+ * (pointers of an empty one are not used) of kinds[i] (TGEMM_IN_*), and
+ * outs[i], of the same kind, may be grads[i] itself.  `norm` is a DEVICE
+ * float.  A norm that is not finite is reported as it is and makes the factor
+ * 0 or NaN, as the formula does.
+ * Requires count >= 1 and every size >= 0 (TGEMM_ERR_DIM), max_norm >= 0 and
+ * eps >= 0, neither a NaN (TGEMM_ERR_VALUE).
+ */
+int ternary_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *sizes,
+                           const int32_t *kinds, int64_t count, float max_norm, float eps, float *norm,
+                           void *workspace, int64_t workspace_bytes, hipStream_t stream);
+int ternary_clip_grad_norm_workspace(const int64_t *sizes, int64_t count, int64_t *bytes);
 
 /* Static description of a status code (never NULL). */
 const char *ternary_gemm_status_str(int status);

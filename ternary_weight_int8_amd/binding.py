@@ -13,9 +13,11 @@ from .build import LIB
 
 OK = 0
 ERR_NULL, ERR_DIM, ERR_PACK, ERR_BOUND, ERR_ALIAS, ERR_HIP, ERR_KIND, ERR_SCRATCH = -1, -2, -3, -4, -5, -6, -7, -8
+ERR_VALUE, ERR_WORKSPACE = -9, -10
 STATIC_SCRATCH_BYTES = 8 << 20   # TGEMM_STATIC_SCRATCH_BYTES
 OUT_F32, OUT_BF16 = 1, 2   # output kinds of the scaled calls
 IN_F32, IN_BF16 = 1, 2     # input kinds of the quantizer calls
+ACTS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu_tanh": 4}   # TGEMM_ACT_*
 
 # entry points declared in include/ternary_gemm.h
 EXPORTS = (
@@ -37,6 +39,14 @@ EXPORTS = (
     "ternary_gemm_s8_dx_scaled_ws",
     "ternary_gemm_dx_workspace",
     "ternary_gemm_s8_dx_noalloc",
+    "ternary_rmsnorm_quantize",
+    "ternary_rmsnorm_backward",
+    "ternary_rmsnorm_backward_workspace",
+    "ternary_gemm_s8_epilogue",
+    "ternary_epilogue_backward",
+    "ternary_epilogue_backward_workspace",
+    "ternary_clip_grad_norm",
+    "ternary_clip_grad_norm_workspace",
 )
 
 OPS = {"fwd": 0, "dx": 1, "dw": 2}
@@ -114,6 +124,19 @@ def lib():
         L.ternary_gemm_s8_dx_noalloc.restype = ctypes.c_int
         L.ternary_gemm_dx_workspace.argtypes = [i64, i64, i64, i64, ctypes.POINTER(i64)]
         L.ternary_gemm_dx_workspace.restype = ctypes.c_int
+        pi64 = ctypes.POINTER(i64)
+        for name, args in (
+                ("ternary_rmsnorm_quantize", [p, i32, p, p, f32, p, p, p, p, p, i64, i64, p]),
+                ("ternary_rmsnorm_backward", [p, p, i32, p, p, p, p, p, i64, i64, p, i64, p]),
+                ("ternary_rmsnorm_backward_workspace", [i64, i64, pi64]),
+                ("ternary_gemm_s8_epilogue", [p, p, p, f32, p, i32, p, p, p, i32, i64, i64, i64, p]),
+                ("ternary_epilogue_backward", [p, p, i32, i32, p, p, p, p, i64, i64, p, i64, p]),
+                ("ternary_epilogue_backward_workspace", [i64, i64, pi64]),
+                ("ternary_clip_grad_norm", [p, p, p, p, i64, f32, f32, p, p, i64, p]),
+                ("ternary_clip_grad_norm_workspace", [p, i64, pi64])):
+            f = getattr(L, name)
+            f.argtypes = args
+            f.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -481,3 +504,220 @@ def ternary_quantize_rows(X, Q=None, scale=None, stream=None):
 def ternary_quantize_cols(X, Q=None, scale=None, stream=None):
     """(Q int8 [R][C], scale float32 [C]): per-column symmetric int8 quantization of X [R][C]."""
     return _quantize("ternary_quantize_cols", X, Q, scale, "cols", stream)
+
+
+# ---------------------------------------------------------------------------
+# the operators around the product: norm, epilogue, their backward passes, and
+# the clipping of gradients
+# ---------------------------------------------------------------------------
+
+def _kind(t, what):
+    """The kind of a float matrix (IN_* and OUT_* have the same values)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{what} must be a float32 or bfloat16 torch.Tensor")
+    return IN_F32 if t.dtype == torch.float32 else IN_BF16
+
+
+def _given(t, dtype, shape, device, what):
+    """An argument that has to have this type, shape and device."""
+    _check(t, dtype, len(shape), what)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    return t
+
+
+def _made(t, dtype, shape, device, what, stream):
+    """The caller's output, or a new one.  A new one comes from the pool of the
+    stream the kernels run on, so that no pending work of another stream still
+    uses its memory."""
+    if t is not None:
+        return _given(t, dtype, shape, device, what)
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(workspace, nbytes, device, stream):
+    """The caller's workspace (a contiguous uint8 device tensor), or a new one."""
+    torch = _torch()
+    if workspace is None:
+        return _made(None, torch.uint8, (nbytes,), device, "workspace", stream)
+    _check(workspace, torch.uint8, 1, "workspace")
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    return workspace
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _done(name, st):
+    if st != OK:
+        raise TernaryGemmError(name, st, status_str(st))
+
+
+def _queried(name, *args):
+    b = ctypes.c_int64()
+    _done(name, getattr(lib(), name)(*args, ctypes.byref(b)))
+    return b.value
+
+
+def _act(act):
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def ternary_rmsnorm_quantize(X, gain, eps=1e-6, residual=None, save=False, H=None, Y=None, rstd=None, Q=None,
+                             scale=None, stream=None):
+    """RMS norm of h = X + residual [R][C] (float32 or bfloat16) into the int8
+    rows that the product takes: (Q int8 [R][C], scale float32 [R], H, Y, rstd).
+
+    H is h in X's type (given as `H`, it may be X or residual; X itself without
+    a residual).  With `save`, Y [R][C] in X's type holds the normed values
+    h * rstd * gain and rstd float32 [R] the rows' 1 / rms, for the backward
+    pass; without, both are None."""
+    torch = _torch()
+    kind = _kind(X, "X")
+    _check(X, X.dtype, 2, "X")
+    (R, C), dt, dev = X.shape, X.dtype, X.device
+    _given(gain, torch.float32, (C,), dev, "gain")
+    if residual is not None:
+        _given(residual, dt, (R, C), dev, "residual")
+        H = _made(H, dt, (R, C), dev, "H", stream)
+    elif H is not None and H is not X:
+        raise ValueError("H is given without a residual: it would be X")
+    if not save and (Y is not None or rstd is not None):
+        raise ValueError("Y and rstd are outputs of save=True")
+    if save:
+        Y = _made(Y, dt, (R, C), dev, "Y", stream)
+        rstd = _made(rstd, torch.float32, (R,), dev, "rstd", stream)
+    Q = _made(Q, torch.int8, (R, C), dev, "Q", stream)
+    scale = _made(scale, torch.float32, (R,), dev, "scale", stream)
+    _done("ternary_rmsnorm_quantize",
+          lib().ternary_rmsnorm_quantize(X.data_ptr(), kind, _ptr(residual), gain.data_ptr(), eps,
+                                         None if residual is None else H.data_ptr(), _ptr(Y), _ptr(rstd),
+                                         Q.data_ptr(), scale.data_ptr(), R, C, _stream(stream, dev)))
+    return Q, scale, X if residual is None else H, Y, rstd
+
+
+def ternary_rmsnorm_backward(dY, H, gain, rstd, dH=None, dX=None, dgain=None, workspace=None, stream=None):
+    """(dX [R][C] in H's type, dgain float32 [C]) from the gradient dY of the
+    normed values, the H and rstd that the norm kept and, with a residual
+    stream, the gradient dH that reaches H past the norm (dX may be dH)."""
+    torch = _torch()
+    kind = _kind(H, "H")
+    _check(H, H.dtype, 2, "H")
+    (R, C), dt, dev = H.shape, H.dtype, H.device
+    _given(dY, dt, (R, C), dev, "dY")
+    _given(gain, torch.float32, (C,), dev, "gain")
+    _given(rstd, torch.float32, (R,), dev, "rstd")
+    if dH is not None:
+        _given(dH, dt, (R, C), dev, "dH")
+    dX = _made(dX, dt, (R, C), dev, "dX", stream)
+    dgain = _made(dgain, torch.float32, (C,), dev, "dgain", stream)
+    ws = _scratch(workspace, _queried("ternary_rmsnorm_backward_workspace", R, C), dev, stream)
+    _done("ternary_rmsnorm_backward",
+          lib().ternary_rmsnorm_backward(dY.data_ptr(), H.data_ptr(), kind, gain.data_ptr(), rstd.data_ptr(),
+                                         _ptr(dH), dX.data_ptr(), dgain.data_ptr(), R, C, ws.data_ptr(), ws.numel(),
+                                         _stream(stream, dev)))
+    return dX, dgain
+
+
+def ternary_gemm_s8_epilogue(A, Wpacked, a_row_scale, w_scale, bias=None, act="none", residual=None, out_dtype=None,
+                             save=False, Y=None, Z=None, stream=None):
+    """(Y, Z): Y [M][N] = act(z) + residual with z = (float(A x W) * a_row_scale[m])
+    * w_scale + bias[n], float32 or bfloat16.  With `save`, Z holds z for the
+    backward pass; without, it is None.  act: none, relu, relu2, silu or
+    gelu_tanh; residual has Y's type and may be Y itself."""
+    torch = _torch()
+    out_dtype = out_dtype or torch.bfloat16
+    _check(A, torch.int8, 2, "A")
+    _check(Wpacked, torch.uint8, 2, "Wpacked")
+    (M, K), dev = A.shape, A.device
+    N = Wpacked.shape[0]
+    _given(Wpacked, torch.uint8, (N, K // 4), dev, "Wpacked")
+    if K % 4:
+        raise ValueError(f"Wpacked must be [N][K/4] = [{N}][{K // 4}], got {tuple(Wpacked.shape)}")
+    _given(a_row_scale, torch.float32, (M,), dev, "a_row_scale")
+    if bias is not None:
+        _given(bias, torch.float32, (N,), dev, "bias")
+    kind, act = _out_kind(out_dtype), _act(act)
+    if residual is not None:
+        _given(residual, out_dtype, (M, N), dev, "residual")
+    if Z is not None and not save:
+        raise ValueError("Z is an output of save=True")
+    Y = _made(Y, out_dtype, (M, N), dev, "Y", stream)
+    if save:
+        Z = _made(Z, out_dtype, (M, N), dev, "Z", stream)
+    _done("ternary_gemm_s8_epilogue",
+          lib().ternary_gemm_s8_epilogue(A.data_ptr(), Wpacked.data_ptr(), a_row_scale.data_ptr(), float(w_scale),
+                                         _ptr(bias), act, _ptr(residual), Y.data_ptr(), _ptr(Z), kind, M, N, K,
+                                         _stream(stream, dev)))
+    return Y, Z
+
+
+def ternary_epilogue_backward(dY, Z, act="none", bias=True, dZ=None, dbias=None, Q=None, scale=None, workspace=None,
+                              stream=None):
+    """(dZ, dbias, Q, scale) from Y's gradient and the saved pre-activation Z
+    [R][C] of the same type: dZ = dY * act'(Z) for dW, its sums over the rows
+    (float32 [C]; None with bias=False), and its int8 rows and scales for dX."""
+    torch = _torch()
+    kind = _kind(Z, "Z")
+    _check(Z, Z.dtype, 2, "Z")
+    (R, C), dt, dev = Z.shape, Z.dtype, Z.device
+    _given(dY, dt, (R, C), dev, "dY")
+    act = _act(act)
+    dZ = _made(dZ, dt, (R, C), dev, "dZ", stream)
+    ws = None
+    if bias:
+        dbias = _made(dbias, torch.float32, (C,), dev, "dbias", stream)
+        ws = _scratch(workspace, _queried("ternary_epilogue_backward_workspace", R, C), dev, stream)
+    elif dbias is not None:
+        raise ValueError("dbias is an output of bias=True")
+    Q = _made(Q, torch.int8, (R, C), dev, "Q", stream)
+    scale = _made(scale, torch.float32, (R,), dev, "scale", stream)
+    _done("ternary_epilogue_backward",
+          lib().ternary_epilogue_backward(dY.data_ptr(), Z.data_ptr(), kind, act, dZ.data_ptr(), _ptr(dbias),
+                                          Q.data_ptr(), scale.data_ptr(), R, C, _ptr(ws),
+                                          0 if ws is None else ws.numel(), _stream(stream, dev)))
+    return dZ, dbias, Q, scale
+
+
+def ternary_clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=None, stream=None):
+    """(out, norm float32 [1]): the gradients scaled by min(1, max_norm / (norm
+    + eps)), norm the root of the sum of all their squares.  grads is a list of
+    contiguous float32 or bfloat16 device tensors of any shapes, on one device;
+    out a list of such tensors (`grads` itself: in place), new ones if None."""
+    torch = _torch()
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    n, dev = len(grads), grads[0].device if isinstance(grads[0], torch.Tensor) else None
+    sizes, kinds = (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+    src, dst = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)()
+    for i, g in enumerate(grads):
+        kinds[i] = _kind(g, f"grads[{i}]")
+        if not g.is_cuda or g.device != dev or not g.is_contiguous():
+            raise ValueError(f"grads[{i}] must be a contiguous tensor on the device of grads[0]")
+        sizes[i], src[i] = g.numel(), g.data_ptr()
+    if out is None:
+        out = [_made(None, g.dtype, tuple(g.shape), dev, "out", stream) for g in grads]
+    elif len(out) != n:
+        raise ValueError(f"out must hold {n} tensors, got {len(out)}")
+    for i, (g, o) in enumerate(zip(grads, out)):
+        if o is not g:
+            _given(o, g.dtype, tuple(g.shape), dev, f"out[{i}]")
+        dst[i] = o.data_ptr()
+    norm = _made(norm, torch.float32, (1,), dev, "norm", stream)
+    ws = _scratch(workspace, _queried("ternary_clip_grad_norm_workspace", sizes, n), dev, stream)
+    _done("ternary_clip_grad_norm",
+          lib().ternary_clip_grad_norm(src, dst, sizes, kinds, n, max_norm, eps, norm.data_ptr(), ws.data_ptr(),
+                                       ws.numel(), _stream(stream, dev)))
+    return out, norm

@@ -7,7 +7,7 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "ternary_gemm.hip")
-SRCS = [SRC, os.path.join(PKG, "csrc", "prep.hip")]
+SRCS = [SRC, os.path.join(PKG, "csrc", "prep.hip"), os.path.join(PKG, "csrc", "block.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libternary_gemm.so")
 # measurement probes for bench.py (a store floor and MFMA-only loops), not

@@ -110,6 +110,9 @@ struct Flag {
 // in IEEE single precision, in that order; bf16 output then rounds y to the
 // nearest bf16, ties to even (v_cvt_pk_bf16_f32; a NaN stays a NaN).
 // ---------------------------------------------------------------------------
+constexpr float kGeluA = 1.5957691216057308f;              // 2 sqrt(2 / pi)
+constexpr float kGeluAB = 1.5957691216057308f * 0.044715f;
+constexpr float kLog2e = 1.4426950408889634f;
 enum OutKind { OUT_I32 = 0, OUT_F32 = TGEMM_OUT_F32, OUT_BF16 = TGEMM_OUT_BF16 };
 static_assert(OUT_F32 != OUT_I32 && OUT_BF16 != OUT_I32 && OUT_F32 != OUT_BF16, "output kinds");
 
@@ -121,7 +124,24 @@ struct Out {
   int32_t kind;       // OutKind
   int32_t vec;        // Cc % 4 == 0 and ptr aligned to 4 elements: 4-element stores
   int32_t vec8;       // bf16, Cc % 8 == 0 and ptr 16-byte aligned: 8-element stores
+  // the epilogue's (Epi below; unused by the plain and scaled calls)
+  const float *bias;  // per output column, or null
+  const void *res;    // [R][Cc] elements of the kind, or null
+  void *z;            // [R][Cc] elements of the kind, or null
+  int32_t act;        // TGEMM_ACT_*
 };
+
+// What the stores of a kernel compute: EPI_NONE the int32 sums or their
+// scaled form; the other two the epilogue of ternary_gemm_s8_epilogue on the
+// scaled sum y, in single precision up to the rounding of what is stored,
+//     z = y + bias[col],   Y = act(z) + res[row][col]
+// with z itself stored too if asked for.  The activations are split in two
+// kinds so that a kernel's unrolled stores hold the code of one kind only:
+// EPI_POLY   none, relu, relu2: a comparison and a product
+// EPI_SIGM   z sigmoid(u(z)), u = z (silu) or a z + b z^3 (gelu's tanh form,
+//            0.5 (1 + tanh(t)) = sigmoid(2 t))
+enum Epi { EPI_NONE = 0, EPI_POLY = 1, EPI_SIGM = 2 };
+int epi_of(int act) { return act == TGEMM_ACT_SILU || act == TGEMM_ACT_GELU_TANH ? EPI_SIGM : EPI_POLY; }
 
 __device__ __forceinline__ float scaled(int32_t x, float r, float c) {
   return __fmul_rn(__fmul_rn((float)x, r), c);
@@ -132,9 +152,99 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
 }
+
+// Element-aligned vectors: the epilogue's loads and stores take any width and
+// any base (gfx950 serves unaligned global accesses), so a row of an odd
+// number of columns still moves four elements at a time.
+typedef float v4f_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t v2u_u __attribute__((ext_vector_type(2), aligned(2)));
+
+template <int E>
+__device__ __forceinline__ float epi_act(float z, int act) {
+#pragma clang fp contract(off)   // every kernel rounds alike
+  if constexpr (E == EPI_POLY) {
+    if (act == TGEMM_ACT_NONE) return z;
+    const float p = z < 0.f ? 0.f : z;   // a NaN stays one
+    return act == TGEMM_ACT_RELU ? p : p * p;
+  } else {
+    // sigmoid(u) = 1 / (1 + 2^t), t = -u log2(e), by the hardware's 2^t and
+    // reciprocal (within 1 ulp each; libm's expf and the IEEE divide made the
+    // unrolled stores spill).  Rounding t leaves a relative error of about
+    // |t| 2^-24 in 2^t, as rounding u does.  Past +-200 the sigmoid is 0 or 1
+    // in single precision; the clamp keeps t finite, and the product with z
+    // brings back a NaN that it drops.
+    const bool silu = act == TGEMM_ACT_SILU;
+    const float k0 = silu ? -kLog2e : -kGeluA * kLog2e, k1 = silu ? 0.f : -kGeluAB * kLog2e;
+    const float c = fminf(fmaxf(z, -200.f), 200.f);
+    const float t = c * __builtin_fmaf(k1, c * c, k0);
+    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t));
+  }
+}
+
+__device__ __forceinline__ void store4(void *base, int32_t kind, int64_t e, const float (&y)[4]) {
+  if (kind == OUT_F32)
+    *reinterpret_cast<v4f_u *>(static_cast<float *>(base) + e) = v4f_u{y[0], y[1], y[2], y[3]};
+  else
+    *reinterpret_cast<v2u_u *>(static_cast<uint16_t *>(base) + e) = v2u_u{bf16_pack(y[0], y[1]), bf16_pack(y[2], y[3])};
+}
+__device__ __forceinline__ void store1(void *base, int32_t kind, int64_t e, float y) {
+  if (kind == OUT_F32)
+    static_cast<float *>(base)[e] = y;
+  else
+    static_cast<uint16_t *>(base)[e] = __builtin_bit_cast(uint16_t, (__bf16)y);
+}
+
+// the epilogue of one element: bias, res and e as the caller fetched them
+template <int E>
+__device__ __forceinline__ void epi_put1(const Out &o, int64_t Cc, int64_t row, int64_t col, int32_t x, float r) {
+#pragma clang fp contract(off)   // every kernel rounds alike
+  const int64_t e = row * Cc + col;
+  float z = scaled(x, r, o.cscal);
+  if (o.bias) z += o.bias[col];
+  if (o.z) store1(o.z, o.kind, e, z);
+  float y = epi_act<E>(z, o.act);
+  if (o.res)
+    y += o.kind == OUT_F32 ? static_cast<const float *>(o.res)[e]
+                           : __uint_as_float((uint32_t)static_cast<const uint16_t *>(o.res)[e] << 16);
+  store1(o.ptr, o.kind, e, y);
+}
+template <int E>
+__device__ __forceinline__ void epi_put4(const Out &o, int64_t Cc, int64_t row, int64_t col, const v4i &v, float r) {
+#pragma clang fp contract(off)   // every kernel rounds alike
+  const int64_t e = row * Cc + col;
+  float y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y[k] = scaled(v[k], r, o.cscal);
+  if (o.bias) {
+    const v4f_u b = *reinterpret_cast<const v4f_u *>(o.bias + col);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] += b[k];
+  }
+  if (o.z) store4(o.z, o.kind, e, y);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y[k] = epi_act<E>(y[k], o.act);
+  if (o.res) {
+    if (o.kind == OUT_F32) {
+      const v4f_u x = *reinterpret_cast<const v4f_u *>(static_cast<const float *>(o.res) + e);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] += x[k];
+    } else {
+      const v2u_u x = *reinterpret_cast<const v2u_u *>(static_cast<const uint16_t *>(o.res) + e);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] += __uint_as_float(k & 1 ? x[k / 2] & 0xFFFF0000u : x[k / 2] << 16);
+    }
+  }
+  store4(o.ptr, o.kind, e, y);
+}
+
 // columns col .. col + 3 of row `row`, all inside the output (o.vec); r is
 // the row's scale (read by the caller; unused for int32)
+template <int E>
 __device__ __forceinline__ void put4(const Out &o, int64_t Cc, int64_t row, int64_t col, const v4i &v, float r) {
+  if constexpr (E != EPI_NONE) {
+    epi_put4<E>(o, Cc, row, col, v, r);
+    return;
+  }
   const int64_t e = row * Cc + col;
   if (o.kind == OUT_I32) {
     *reinterpret_cast<v4i *>(static_cast<int32_t *>(o.ptr) + e) = v;
@@ -152,7 +262,12 @@ __device__ __forceinline__ void put4(const Out &o, int64_t Cc, int64_t row, int6
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o.ptr) + e) = b;
   }
 }
+template <int E>
 __device__ __forceinline__ void put1(const Out &o, int64_t Cc, int64_t row, int64_t col, int32_t x, float r) {
+  if constexpr (E != EPI_NONE) {
+    epi_put1<E>(o, Cc, row, col, x, r);
+    return;
+  }
   const int64_t e = row * Cc + col;
   if (o.kind == OUT_I32) {
     static_cast<int32_t *>(o.ptr)[e] = x;
@@ -746,7 +861,7 @@ struct StageBytes {
 // Epilogue: lane holds O[row][col .. col+3] of each 16x16 block of a wave's
 // sub-tile starting at (r0, c0); `inside` says the workgroup's whole tile is
 // inside the output.
-template <class T>
+template <class T, int E = EPI_NONE>
 __device__ __forceinline__ void store_tile(const Args &a, const v4i (&acc)[T::FM][T::FN], int64_t r0,
                                            int64_t c0, bool inside, int lane) {
   const int64_t rbase = r0 + (lane & 15);
@@ -768,7 +883,7 @@ __device__ __forceinline__ void store_tile(const Args &a, const v4i (&acc)[T::FM
         v4i v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_ds_bpermute(src, acc[i][j][e]);
-        put4(a.o, a.Cc, row, cp + j * 16, v, r);
+        put4<E>(a.o, a.Cc, row, cp + j * 16, v, r);
       }
     }
     return;
@@ -782,17 +897,17 @@ __device__ __forceinline__ void store_tile(const Args &a, const v4i (&acc)[T::FM
     for (int j = 0; j < T::FN; ++j) {
       const int64_t col = cbase + j * 16;
       if (a.o.vec && col + 3 < a.Cc) {
-        put4(a.o, a.Cc, row, col, acc[i][j], r);
+        put4<E>(a.o, a.Cc, row, col, acc[i][j], r);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (col + e < a.Cc) put1(a.o, a.Cc, row, col + e, acc[i][j][e], r);
+          if (col + e < a.Cc) put1<E>(a.o, a.Cc, row, col + e, acc[i][j][e], r);
       }
     }
   }
 }
 
-template <int OP, class T, bool FAST>
+template <int OP, class T, bool FAST, int E = EPI_NONE>
 __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads), amdgpu_waves_per_eu(T::OCC)))
 void tgemm_kernel(Args a) {
   typedef StageBytes<OP, T> SB;
@@ -857,7 +972,7 @@ void tgemm_kernel(Args a) {
   for (; g < gfull; ++g) group(g, Flag<true>());
   for (; g < ngroups; ++g) group(g, Flag<false>());
 
-  store_tile<T>(a, acc, q0 + wm * T::TM, p0 + wn * T::TN, q0 + T::BM <= a.R && p0 + T::BN <= a.Cc,
+  store_tile<T, E>(a, acc, q0 + wm * T::TM, p0 + wn * T::TN, q0 + T::BM <= a.R && p0 + T::BN <= a.Cc,
                 lane);
 }
 
@@ -1290,7 +1405,7 @@ __device__ __forceinline__ void fs_decode_write(const uint32_t (&x)[fs::Geo<OP>:
     }
 }
 
-template <int OP>
+template <int OP, int E = EPI_NONE>
 __global__ __attribute__((amdgpu_flat_work_group_size(fs::kNT, fs::kNT), amdgpu_waves_per_eu(2)))
 void tgemm_stream(SArgs a) {
   using namespace fs;
@@ -1511,7 +1626,7 @@ void tgemm_stream(SArgs a) {
     // a one-step tile has not waited for anything issued after its row scales
     if (scaled_out && a.nk < 2) wait_vm<0>();
     const float *rsw = rs_s + TM * wave;
-    if (a.o.vec8 && m0 + BM <= a.R && n0 + BN <= a.Cc) {
+    if (E == EPI_NONE && a.o.vec8 && m0 + BM <= a.R && n0 + BN <= a.Cc) {
       // bf16: scale and convert in the MFMA layout (lane l: row l % 16, four
       // columns -> two dwords), then give each lane 8 columns of a fragment
       // pair's 32: lane L takes row L / 4, columns 8 (L % 4) .. + 7 (fragment
@@ -1570,7 +1685,7 @@ void tgemm_stream(SArgs a) {
           v4i v;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_ds_bpermute(src, acc[i][jj][e]);
-          put4(a.o, a.Cc, rp + 16 * i, cp + 16 * jj, v, r);
+          put4<E>(a.o, a.Cc, rp + 16 * i, cp + 16 * jj, v, r);
         }
       }
       after = G::kStores;
@@ -1584,11 +1699,11 @@ void tgemm_stream(SArgs a) {
         for (int jj = 0; jj < FN; ++jj) {
           const int32_t col = cb + 16 * jj;
           if (a.o.vec && col + 3 < a.Cc) {
-            put4(a.o, a.Cc, row, col, acc[i][jj], r);
+            put4<E>(a.o, a.Cc, row, col, acc[i][jj], r);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (col + e < a.Cc) put1(a.o, a.Cc, row, col + e, acc[i][jj][e], r);
+              if (col + e < a.Cc) put1<E>(a.o, a.Cc, row, col + e, acc[i][jj][e], r);
           }
         }
       }
@@ -1716,7 +1831,7 @@ __device__ __forceinline__ void sk_step(v4i (&acc)[MF][NB], const v4i (&w)[NB], 
 // eight waves, in wave order, and stores it at output row m, columns
 // c0 + 4 (t % (4 NB)) .. + 3 of a row-major output with `width` columns:
 // neighbouring threads write neighbouring 16-byte pieces of one output row.
-template <int MF, int NB>
+template <int MF, int NB, int E = EPI_NONE>
 __device__ __forceinline__ void sk_epilogue(int8_t *smem, const v4i (&acc)[MF][NB], const Out &o, int wave, int lane,
                                             int tid, int32_t c0, int32_t M, int32_t width) {
   constexpr int kPitch = 4 * NB + 1, kWave = 16 * MF * kPitch;
@@ -1739,17 +1854,17 @@ __device__ __forceinline__ void sk_epilogue(int8_t *smem, const v4i (&acc)[MF][N
     if (m < M) {
       const float rsc = row_scale(o, m);
       if (o.vec && col + 3 < width) {
-        put4(o, width, m, col, sum, rsc);
+        put4<E>(o, width, m, col, sum, rsc);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (col + e < width) put1(o, width, m, col + e, sum[e], rsc);
+          if (col + e < width) put1<E>(o, width, m, col + e, sum[e], rsc);
       }
     }
   }
 }
 
-template <int MF, int NB, bool AL>
+template <int MF, int NB, bool AL, int E = EPI_NONE>
 __global__ __attribute__((amdgpu_flat_work_group_size(sk::kNT, sk::kNT), amdgpu_waves_per_eu(2)))
 void tgemm_skinny(KArgs a) {
   typedef SkLds<MF, NB, AL> L;
@@ -1824,7 +1939,7 @@ void tgemm_skinny(KArgs a) {
   // partial sums -> LDS; with AL the buffer reuses the A tiles, once every
   // wave is done with them
   if constexpr (AL) __syncthreads();
-  sk_epilogue<MF, NB>(smem, acc, a.o, wave, lane, tid, n0, a.M, a.N);
+  sk_epilogue<MF, NB, E>(smem, acc, a.o, wave, lane, tid, n0, a.M, a.N);
 }
 
 // ---------------------------------------------------------------------------
@@ -2109,25 +2224,24 @@ __global__ __launch_bounds__(256) void skinny_dx_sum(const v4i *__restrict__ par
     const int64_t row = i / kq, col = 4 * (i % kq);
     const float rsc = row_scale(o, row);
     if (o.vec) {
-      put4(o, K, row, col, t, rsc);
+      put4<EPI_NONE>(o, K, row, col, t, rsc);
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) put1(o, K, row, col + k, t[k], rsc);
+      for (int k = 0; k < 4; ++k) put1<EPI_NONE>(o, K, row, col + k, t[k], rsc);
     }
   }
 }
 
-template <int OP, class T, bool FAST>
+template <int OP, class T, bool FAST, int E>
 hipError_t launch_t(const Args &a, hipStream_t stream) {
-  hipLaunchKernelGGL((tgemm_kernel<OP, T, FAST>), dim3(a.tiles), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((tgemm_kernel<OP, T, FAST, E>), dim3(a.tiles), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
-template <int OP, class T>
+template <int OP, class T, int E>
 hipError_t launch_f(const Args &a, bool fast, hipStream_t stream) {
-  return fast ? launch_t<OP, T, true>(a, stream) : launch_t<OP, T, false>(a, stream);
+  return fast ? launch_t<OP, T, true, E>(a, stream) : launch_t<OP, T, false, E>(a, stream);
 }
-
 
 // Kernel per product, tile and load path:
 //   tiled  tgemm_kernel: every case but the next
@@ -2284,9 +2398,15 @@ void launch_skinny_dx(const XArgs &xa, int grid, hipStream_t stream) {
   hipLaunchKernelGGL((tgemm_skinny_dx<MF, NB>), dim3(grid), dim3(sk::kNT), 0, stream, xa);
 }
 
+template <int MF, int NB, bool AL, int E>
+void launch_skinny_e(const KArgs &ka, int grid, hipStream_t stream) {
+  hipLaunchKernelGGL((tgemm_skinny<MF, NB, AL, E>), dim3(grid), dim3(sk::kNT), 0, stream, ka);
+}
 template <int MF, int NB, bool AL>
-void launch_skinny(const KArgs &ka, int grid, hipStream_t stream) {
-  hipLaunchKernelGGL((tgemm_skinny<MF, NB, AL>), dim3(grid), dim3(sk::kNT), 0, stream, ka);
+void launch_skinny(const KArgs &ka, int grid, int epi, hipStream_t stream) {
+  if (epi == EPI_NONE) launch_skinny_e<MF, NB, AL, EPI_NONE>(ka, grid, stream);
+  else if (epi == EPI_POLY) launch_skinny_e<MF, NB, AL, EPI_POLY>(ka, grid, stream);
+  else launch_skinny_e<MF, NB, AL, EPI_SIGM>(ka, grid, stream);
 }
 
 // the contraction split between two halves of a workgroup: dW on the
@@ -2315,7 +2435,7 @@ int kernel_lds(int op, int kernel, int tile) {
                     : lds_of_kernel<DW>(kernel, tile);
 }
 
-template <int OP>
+template <int OP, int E = EPI_NONE>
 hipError_t launch_op(const Args &a, int kernel, int tile, bool fast, hipStream_t stream) {
   if constexpr (OP == DW || OP == DX) {
     if (kernel == KSPLIT) {
@@ -2328,18 +2448,26 @@ hipError_t launch_op(const Args &a, int kernel, int tile, bool fast, hipStream_t
     }
   }
   switch (tile) {
-    case TL: return launch_f<OP, typename Tiles<OP>::L>(a, fast, stream);
-    case TW: return launch_f<OP, typename Tiles<OP>::W>(a, fast, stream);
-    default: return launch_f<OP, typename Tiles<OP>::S>(a, fast, stream);
+    case TL: return launch_f<OP, typename Tiles<OP>::L, E>(a, fast, stream);
+    case TW: return launch_f<OP, typename Tiles<OP>::W, E>(a, fast, stream);
+    default: return launch_f<OP, typename Tiles<OP>::S, E>(a, fast, stream);
   }
 }
 
+// what ternary_gemm_s8_epilogue adds to the scaled forward
+struct EpiArgs {
+  const float *bias;
+  const void *res;
+  void *z;
+  int32_t act;
+};
+
 // out: the output buffer, elements of `kind`; rs, cs, cscal: the scales of
 // the scaled kinds (rs per output row; cs per output column, or null and
-// cscal for every column)
+// cscal for every column); ep: the epilogue (forward, scaled kinds), or null
 int run(int op, const int8_t *q, const void *p, void *out, int kind, const float *rs, const float *cs,
         float cscal, int64_t M, int64_t N, int64_t K, hipStream_t stream, void *ws = nullptr,
-        int64_t ws_bytes = 0) {
+        int64_t ws_bytes = 0, const EpiArgs *ep = nullptr) {
   const int st = check_dims(op, M, N, K);
   if (st != TGEMM_OK) return st;
   const Shape s = shape_of(op, M, N, K);
@@ -2357,8 +2485,21 @@ int run(int op, const int8_t *q, const void *p, void *out, int kind, const float
       (overlaps(ws, ws_bytes, q, qbytes) || overlaps(ws, ws_bytes, p, pbytes) ||
        overlaps(ws, ws_bytes, out, obytes) || (kind != OUT_I32 && overlaps(ws, ws_bytes, rs, s.R * 4))))
     return TGEMM_ERR_ALIAS;
+  if (ep) {
+    // the residual may be the output itself, element for element (each
+    // element is read by the thread that then writes it); nothing else overlaps
+    const bool in_place = ep->res == out;
+    if (ep->bias && overlaps(out, obytes, ep->bias, N * 4)) return TGEMM_ERR_ALIAS;
+    if (ep->res && !in_place && overlaps(out, obytes, ep->res, obytes)) return TGEMM_ERR_ALIAS;
+    if (ep->z && (overlaps(ep->z, obytes, out, obytes) || overlaps(ep->z, obytes, q, qbytes) ||
+                  overlaps(ep->z, obytes, p, pbytes) || overlaps(ep->z, obytes, rs, s.R * 4) ||
+                  (ep->bias && overlaps(ep->z, obytes, ep->bias, N * 4)) ||
+                  (ep->res && overlaps(ep->z, obytes, ep->res, obytes))))
+      return TGEMM_ERR_ALIAS;
+  }
   Machine mc;
   if (query_machine(&mc) != TGEMM_OK) return TGEMM_ERR_HIP;
+  const int epi = ep ? epi_of(ep->act) : EPI_NONE;
   Out o;
   o.ptr = out;
   o.rs = rs;
@@ -2367,6 +2508,17 @@ int run(int op, const int8_t *q, const void *p, void *out, int kind, const float
   o.kind = kind;
   o.vec = (s.Cc % 4 == 0 && aligned(out, 4 * esz)) ? 1 : 0;
   o.vec8 = (kind == OUT_BF16 && s.Cc % 8 == 0 && aligned(out, 16)) ? 1 : 0;
+  o.bias = nullptr;
+  o.res = nullptr;
+  o.z = nullptr;
+  o.act = TGEMM_ACT_NONE;
+  if (ep) {
+    o.vec = 1;   // element-aligned vectors: any width, any base
+    o.bias = ep->bias;
+    o.res = ep->res;
+    o.z = ep->z;
+    o.act = ep->act;
+  }
 
   const int tile = pick_tile_for(op, s, mc.cus);
   const TileInfo &ti = kTileInfo[tile];
@@ -2400,15 +2552,15 @@ int run(int op, const int8_t *q, const void *p, void *out, int kind, const float
       ka.vq = (int32_t)(K % sk::SK / BK);
       const int sel = 100 * kp.mf + 10 * kp.nb + (kp.al ? 1 : 0);
       switch (sel) {
-        case 110: launch_skinny<1, 1, false>(ka, kp.grid, stream); break;
-        case 120: launch_skinny<1, 2, false>(ka, kp.grid, stream); break;
-        case 140: launch_skinny<1, 4, false>(ka, kp.grid, stream); break;
-        case 111: launch_skinny<1, 1, true>(ka, kp.grid, stream); break;
-        case 121: launch_skinny<1, 2, true>(ka, kp.grid, stream); break;
-        case 141: launch_skinny<1, 4, true>(ka, kp.grid, stream); break;
-        case 211: launch_skinny<2, 1, true>(ka, kp.grid, stream); break;
-        case 221: launch_skinny<2, 2, true>(ka, kp.grid, stream); break;
-        default: launch_skinny<2, 4, true>(ka, kp.grid, stream); break;
+        case 110: launch_skinny<1, 1, false>(ka, kp.grid, epi, stream); break;
+        case 120: launch_skinny<1, 2, false>(ka, kp.grid, epi, stream); break;
+        case 140: launch_skinny<1, 4, false>(ka, kp.grid, epi, stream); break;
+        case 111: launch_skinny<1, 1, true>(ka, kp.grid, epi, stream); break;
+        case 121: launch_skinny<1, 2, true>(ka, kp.grid, epi, stream); break;
+        case 141: launch_skinny<1, 4, true>(ka, kp.grid, epi, stream); break;
+        case 211: launch_skinny<2, 1, true>(ka, kp.grid, epi, stream); break;
+        case 221: launch_skinny<2, 2, true>(ka, kp.grid, epi, stream); break;
+        default: launch_skinny<2, 4, true>(ka, kp.grid, epi, stream); break;
       }
       static_assert(SkLds<2, 4, true>::kBytes == 8 * 32 * 17 * 16 && SkLds<1, 1, true>::kBytes == 8 * 16 * 256,
                     "plan LDS");
@@ -2474,7 +2626,11 @@ int run(int op, const int8_t *q, const void *p, void *out, int kind, const float
       sa.tiles_c = sp.tiles_c;
       sa.tiles = sp.tiles;
       sa.nk = (int32_t)(s.L / BK);
-      if (op == FWD)
+      if (epi == EPI_POLY)
+        hipLaunchKernelGGL((tgemm_stream<FWD, EPI_POLY>), dim3(sp.grid), dim3(fs::kNT), 0, stream, sa);
+      else if (epi == EPI_SIGM)
+        hipLaunchKernelGGL((tgemm_stream<FWD, EPI_SIGM>), dim3(sp.grid), dim3(fs::kNT), 0, stream, sa);
+      else if (op == FWD)
         hipLaunchKernelGGL(tgemm_stream<FWD>, dim3(sp.grid), dim3(fs::kNT), 0, stream, sa);
       else
         hipLaunchKernelGGL(tgemm_stream<DX>, dim3(sp.grid), dim3(fs::kNT), 0, stream, sa);
@@ -2484,7 +2640,11 @@ int run(int op, const int8_t *q, const void *p, void *out, int kind, const float
 
   const int kernel = pick_kernel(op, tile, s.L, a.tiles, mc);
   hipError_t e;
-  if (op == FWD)
+  if (epi == EPI_POLY)
+    e = launch_op<FWD, EPI_POLY>(a, kernel, tile, fast, stream);
+  else if (epi == EPI_SIGM)
+    e = launch_op<FWD, EPI_SIGM>(a, kernel, tile, fast, stream);
+  else if (op == FWD)
     e = launch_op<FWD>(a, kernel, tile, fast, stream);
   else if (op == DX)
     e = launch_op<DX>(a, kernel, tile, fast, stream);
@@ -2545,6 +2705,16 @@ int ternary_gemm_s8_scaled(const int8_t *A, const uint8_t *Wpacked, const float 
   if (!A || !Wpacked || !a_row_scale || !Y) return TGEMM_ERR_NULL;
   if (out_kind != TGEMM_OUT_F32 && out_kind != TGEMM_OUT_BF16) return TGEMM_ERR_KIND;
   return run(FWD, A, Wpacked, Y, out_kind, a_row_scale, nullptr, w_scale, M, N, K, stream);
+}
+
+int ternary_gemm_s8_epilogue(const int8_t *A, const uint8_t *Wpacked, const float *a_row_scale, float w_scale,
+                             const float *bias, int act, const void *residual, void *Y, void *Z, int out_kind,
+                             int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  if (!A || !Wpacked || !a_row_scale || !Y) return TGEMM_ERR_NULL;
+  if (out_kind != TGEMM_OUT_F32 && out_kind != TGEMM_OUT_BF16) return TGEMM_ERR_KIND;
+  if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_VALUE;
+  const EpiArgs ep = {bias, residual, Z, act};
+  return run(FWD, A, Wpacked, Y, out_kind, a_row_scale, nullptr, w_scale, M, N, K, stream, nullptr, 0, &ep);
 }
 
 int ternary_gemm_s8_dx_scaled(const int8_t *dC, const uint8_t *Wpacked, const float *dc_row_scale,
@@ -2620,6 +2790,8 @@ const char *ternary_gemm_status_str(int status) {
     case TGEMM_ERR_HIP: return "the HIP runtime reported an error at launch";
     case TGEMM_ERR_KIND: return "the output kind is not TGEMM_OUT_F32 or TGEMM_OUT_BF16";
     case TGEMM_ERR_SCRATCH: return "the split needs more scratch than the library's static buffer holds";
+    case TGEMM_ERR_VALUE: return "a scalar argument (eps, max_norm, act) is out of its range";
+    case TGEMM_ERR_WORKSPACE: return "the workspace is NULL, too small or not 16-byte aligned";
     default: return "unknown status";
   }
 }
