@@ -29,6 +29,8 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kNT = 256;   // threads per workgroup
+constexpr int64_t kCUs = 256;                        // compute units of an MI355X
+constexpr int64_t kNormWaves = 32, kBwdWaves = 8;    // waves a CU of the row kernels' grids, at most
 
 bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
@@ -78,6 +80,200 @@ __device__ __forceinline__ float block_max(uint32_t v, uint32_t *part) {
 #pragma unroll
   for (int i = 1; i < kNT / 64; ++i) m = part[i] > m ? part[i] : m;
   return __uint_as_float(m);
+}
+
+// ---------------------------------------------------------------------------
+// Rows held in registers.  The three row operators need a sum or a maximum
+// over a row before they can write it, so a row is read once into registers,
+// reduced, and written from them: HBM sees every input and output once.
+//
+// NT threads share a row (a wave, four waves or sixteen), each holding V units
+// of 16 bytes (U elements): unit j of thread t is unit t + NT j of the row, so
+// a wave's loads cover whole lines.  Rows need not be whole units or aligned:
+// loads and stores are element-aligned vectors (gfx950 serves them), and the
+// row's last unit is the last U elements, of which the first `dup` also
+// belong to the unit before; both threads compute and store the same values
+// for them, and only the row's sums and the column sums leave them out.  (A
+// store never precedes the reduction that every load of the row precedes, so
+// this holds for in-place outputs too.)  Rows of fewer than U elements, and
+// rows that no NT, V holds, take the looped kernels further down.
+// ---------------------------------------------------------------------------
+template <class T>
+constexpr int kU = 16 / (int)sizeof(T);
+
+template <class T>
+struct Raw;
+template <>
+struct Raw<float> {
+  typedef float V __attribute__((ext_vector_type(4), aligned(4)));
+};
+template <>
+struct Raw<uint16_t> {
+  typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
+};
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32u __attribute__((aligned(1)));
+
+__device__ __forceinline__ void unpack(const Raw<float>::V &r, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = r[i];
+}
+__device__ __forceinline__ void unpack(const Raw<uint16_t>::V &r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(r[i] << 16);
+    v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ Raw<float>::V pack(const float (&v)[4]) { return {v[0], v[1], v[2], v[3]}; }
+__device__ __forceinline__ Raw<uint16_t>::V pack(const float (&v)[8]) {
+  Raw<uint16_t>::V r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){v[2 * i], v[2 * i + 1]}, bf16x2));
+  return r;
+}
+
+// Workgroup barrier for LDS only (outstanding global loads and stores go on)
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Sum and maximum over a wave, the same in every lane: pairs, quads, eights
+// and sixteens by data-parallel moves, then the four sixteens through scalar
+// registers.  Every lane has to be active.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+__device__ __forceinline__ float lane_f(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += __uint_as_float(dpp<kXor1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kXor2>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kHalfMirror>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kMirror>(__float_as_uint(v)));
+  return (lane_f(v, 0) + lane_f(v, 16)) + (lane_f(v, 32) + lane_f(v, 48));
+}
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = umax(v, dpp<kXor1>(v));
+  v = umax(v, dpp<kXor2>(v));
+  v = umax(v, dpp<kHalfMirror>(v));
+  v = umax(v, dpp<kMirror>(v));
+  const uint32_t a = __builtin_amdgcn_readlane((int)v, 0), b = __builtin_amdgcn_readlane((int)v, 16);
+  const uint32_t c = __builtin_amdgcn_readlane((int)v, 32), d = __builtin_amdgcn_readlane((int)v, 48);
+  return umax(umax(a, b), umax(c, d));
+}
+// over the NT threads of a row: a wave by itself, or the workgroup's NT / 64
+// waves through `part` (one word a wave).  One barrier: a caller alternates
+// between two `part`s from row to row, and the barrier of the row between
+// separates the reads of one from the next writes to it.
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, float *part) {
+  v = wave_sum(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    lds_barrier();
+    v = part[0];
+#pragma unroll
+    for (int i = 1; i < NT / 64; ++i) v += part[i];
+  }
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ float row_max(uint32_t v, uint32_t *part) {
+  v = wave_max(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    lds_barrier();
+    v = part[0];
+#pragma unroll
+    for (int i = 1; i < NT / 64; ++i) v = umax(v, part[i]);
+  }
+  return __uint_as_float(v);
+}
+
+// A thread's units of a row of C elements
+template <class T, int NT, int V>
+struct Units {
+  static constexpr int U = kU<T>;
+  int off[V];    // first element of each unit
+  int32_t dup;   // of the row's last unit: elements that the unit before has too
+  int32_t last;  // j of the thread's unit if that is the row's last and dup > 0, else -1
+  int32_t n;     // units of the thread
+  __device__ __forceinline__ void init(int32_t C, int t) {
+    const int32_t nu = (C + U - 1) / U;
+    dup = nu * U - C;
+    last = dup && (nu - 1) % NT == t ? (nu - 1) / NT : -1;
+    n = t < nu ? (nu - 1 - t) / NT + 1 : 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int32_t o = (t + NT * j) * U;
+      off[j] = o + U <= C ? o : C - U;
+    }
+  }
+  __device__ __forceinline__ bool on(int j) const { return j < n; }
+};
+
+template <class T>
+__device__ __forceinline__ typename Raw<T>::V load_raw(const T *p) {
+  return *reinterpret_cast<const typename Raw<T>::V *>(p);
+}
+template <class T>
+__device__ __forceinline__ void store_raw(T *p, const typename Raw<T>::V &v) {
+  *reinterpret_cast<typename Raw<T>::V *>(p) = v;
+}
+template <int U>
+__device__ __forceinline__ void load_f(const float *p, float (&v)[U]) {
+#pragma unroll
+  for (int i = 0; i < U; i += 4) {
+    const Raw<float>::V r = load_raw(p + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[i + k] = r[k];
+  }
+}
+
+// Int8 rows.  With s >= max|y| / 127 rounded and r = 1 / s rounded, the
+// quotient y / s correctly rounded takes two corrections of y r (the second
+// starts within one unit in the last place, from which one correction with a
+// correctly rounded reciprocal is exact); 1.5 2^23 added to it leaves the
+// nearest whole number, ties to even, in the low bits, and |y / s| <= 127.0001
+// needs no clamp.  That is the IEEE division and rint of the row quantizer in
+// six operations where s and r are well inside the normal range (fast_scale);
+// elsewhere quant1 divides.
+__device__ __forceinline__ bool fast_scale(float s) { return s >= 0x1p-100f && s <= 0x1p120f; }
+template <int U>
+__device__ __forceinline__ void store_q(int8_t *q, const float (&y)[U], float s, float r, bool fast) {
+  uint32_t w[U / 4];
+  if (fast) {
+#pragma unroll
+    for (int k = 0; k < U / 4; ++k) {
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = y[4 * k + i];
+        float p = v * r;
+        p = __builtin_fmaf(__builtin_fmaf(-p, s, v), r, p);
+        p = __builtin_fmaf(__builtin_fmaf(-p, s, v), r, p);
+        b[i] = __float_as_uint(p + 12582912.f);
+      }
+      // bytes 0 of b[0], b[1] and of b[2], b[3], then the two halves
+      const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
+      w[k] = lo | hi;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < U / 4; ++k) {
+      w[k] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[k] |= (uint32_t)(uint8_t)quant1(y[4 * k + i], s) << (8 * i);
+    }
+  }
+  if constexpr (U == 8)
+    *reinterpret_cast<u32x2u *>(q) = u32x2u{w[0], w[1]};
+  else
+    *reinterpret_cast<u32u *>(q) = w[0];
 }
 
 // ---------------------------------------------------------------------------
@@ -138,17 +334,220 @@ __global__ __launch_bounds__(kNT) void norm_rows(NormArgs a) {
   }
 }
 
+// rows in registers, grid-stride over groups of NT threads; the gain stays in
+// registers from row to row
+template <class T, int NT, int V, int BT>
+__global__ __launch_bounds__(BT) void norm_reg(NormArgs a) {
+  constexpr int U = kU<T>;
+  __shared__ float part[2][BT / 64];
+  __shared__ uint32_t upart[2][BT / 64];
+  const int t = threadIdx.x & (NT - 1);
+  const int grp = NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  constexpr int kGroups = BT / NT;
+  static_assert(NT == 64 || NT == BT, "a wave or the workgroup");
+  Units<T, NT, V> un;
+  un.init((int32_t)a.C, t);
+  float gain[V][U];
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (un.on(j)) load_f<U>(a.gain + un.off[j], gain[j]);
+  int flip = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kGroups + grp; row < a.R; row += (int64_t)gridDim.x * kGroups, flip ^= 1) {
+    const int64_t base = row * a.C;
+    const T *x = static_cast<const T *>(a.X) + base;
+    typename Raw<T>::V h[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) h[j] = load_raw(x + un.off[j]);
+    if (a.res) {
+      const T *res = static_cast<const T *>(a.res) + base;
+      typename Raw<T>::V r[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) r[j] = load_raw(res + un.off[j]);
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) {
+          float f[U], g[U];
+          unpack(h[j], f);
+          unpack(r[j], g);
+#pragma unroll
+          for (int i = 0; i < U; ++i) f[i] += g[i];
+          h[j] = pack(f);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        float f[U];
+        unpack(h[j], f);
+        if (j == un.last) {
+#pragma unroll
+          for (int i = 0; i < U; ++i) f[i] = i < un.dup ? 0.f : f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) ss = __builtin_fmaf(f[i], f[i], ss);
+      }
+    ss = row_sum<NT>(ss, part[flip]);
+    const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ss, (float)a.C) + a.eps));
+    if (a.res) {
+      T *H = static_cast<T *>(a.H) + base;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) store_raw(H + un.off[j], h[j]);
+    }
+    float y[V][U];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        unpack(h[j], y[j]);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          y[j][i] = (y[j][i] * rstd) * gain[j][i];
+          m = umax(m, mag(y[j][i]));
+        }
+      }
+    const float s = __fdiv_rn(row_max<NT>(m, upart[flip]), 127.f), r = __fdiv_rn(1.f, s);
+    const bool fast = fast_scale(s);
+    if (t == 0) {
+      a.scale[row] = s;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    int8_t *q = a.Q + base;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) store_q<U>(q + un.off[j], y[j], s, r, fast);
+    if (a.Y) {
+      T *Y = static_cast<T *>(a.Y) + base;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) store_raw(Y + un.off[j], pack(y[j]));
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
-// Backward of the norm, and of the epilogue: a pass over rows, and one over
-// columns for the gradients that are sums over rows.
+// Backward of the norm, and of the epilogue.  In registers: one pass over the
+// rows, each thread adding its columns' terms up over the rows that its group
+// takes; the sums of a workgroup's groups meet in LDS, and its row of P goes
+// to col_finish, which adds the workgroups up in order.
 // ---------------------------------------------------------------------------
+template <class T, int NT, int V, int BT>
+__device__ __forceinline__ void write_cols(float (&acc)[V][kU<T>], const Units<T, NT, V> &un, int grp, float *lds,
+                                           float *__restrict__ P) {
+  constexpr int U = kU<T>;
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (j != un.last || i >= un.dup) f(un.off[j] + i, acc[j][i]);
+      }
+  };
+  if constexpr (NT == BT) {
+    each([&](int c, float v) { P[c] = v; });
+  } else {
+    // group after group adds into LDS
+    for (int g = 0; g < BT / NT; ++g) {
+      if (grp == g) {
+        if (g == 0)
+          each([&](int c, float v) { lds[c] = v; });
+        else if (g < BT / NT - 1)
+          each([&](int c, float v) { lds[c] += v; });
+        else
+          each([&](int c, float v) { P[c] = lds[c] + v; });
+      }
+      lds_barrier();
+    }
+  }
+}
+
 struct NormBwdArgs {
   const void *dY, *H;
   const float *gain, *rstd;
   const void *dH;
   void *dX;
+  float *P;      // [gridDim.x][C]
   int64_t R, C;
 };
+
+template <class T, int NT, int V, int BT>
+__global__ __launch_bounds__(BT) void norm_bwd_reg(NormBwdArgs a) {
+  constexpr int U = kU<T>, kGroups = BT / NT;
+  __shared__ float part[2][BT / 64];
+  __shared__ float cols[NT == BT ? 1 : NT * V * U];
+  const int t = threadIdx.x & (NT - 1);
+  const int grp = NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  Units<T, NT, V> un;
+  un.init((int32_t)a.C, t);
+  float gain[V][U], acc[V][U];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (un.on(j)) load_f<U>(a.gain + un.off[j], gain[j]);
+#pragma unroll
+    for (int i = 0; i < U; ++i) acc[j][i] = 0.f;
+  }
+  const float invC = __fdiv_rn(1.f, (float)a.C);
+  int flip = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kGroups + grp; row < a.R; row += (int64_t)gridDim.x * kGroups, flip ^= 1) {
+    const int64_t base = row * a.C;
+    typename Raw<T>::V dy[V], h[V], dh[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        dy[j] = load_raw(static_cast<const T *>(a.dY) + base + un.off[j]);
+        h[j] = load_raw(static_cast<const T *>(a.H) + base + un.off[j]);
+      }
+    if (a.dH) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) dh[j] = load_raw(static_cast<const T *>(a.dH) + base + un.off[j]);
+    }
+    const float rstd = a.rstd[row];
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        float d[U], f[U], part_sum = 0.f;
+        unpack(dy[j], d);
+        unpack(h[j], f);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const float g = d[i] * (f[i] * rstd);
+          acc[j][i] += g;
+          part_sum = __builtin_fmaf(g, (j == un.last && i < un.dup) ? 0.f : gain[j][i], part_sum);
+        }
+        sum += part_sum;
+      }
+    if (NT > 64 && a.dH) {
+      // dX may be dH itself, and two waves may share a row's last elements:
+      // dH is in registers before the barrier that the stores come after
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) asm volatile("" : "+v"(dh[j]));
+    }
+    const float mean = row_sum<NT>(sum, part[flip]) * invC;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        float d[U], f[U];
+        unpack(dy[j], d);
+        unpack(h[j], f);
+#pragma unroll
+        for (int i = 0; i < U; ++i) d[i] = rstd * __builtin_fmaf(-(f[i] * rstd), mean, d[i] * gain[j][i]);
+        if (a.dH) {
+          unpack(dh[j], f);
+#pragma unroll
+          for (int i = 0; i < U; ++i) d[i] += f[i];
+        }
+        store_raw(static_cast<T *>(a.dX) + base + un.off[j], pack(d));
+      }
+  }
+  write_cols<T, NT, V, BT>(acc, un, grp, cols, a.P + (int64_t)blockIdx.x * a.C);
+}
 
 template <class T>
 __global__ __launch_bounds__(kNT) void norm_bwd_rows(NormBwdArgs a) {
@@ -176,6 +575,7 @@ struct EpiBwdArgs {
   void *dZ;
   int8_t *Q;
   float *scale;
+  float *P;      // [gridDim.x][C], or null
   int64_t R, C;
   int32_t act;
 };
@@ -199,6 +599,58 @@ __device__ __forceinline__ float back(float dy, float z, int act) {
   const float e = __builtin_amdgcn_exp2f(fminf(-u * kLog2e, 126.f));
   const float p = __builtin_amdgcn_rcpf(1.f + e);
   return dy * (p + c * p * (e * p) * du);
+}
+
+template <class T, int NT, int V, int BT>
+__global__ __launch_bounds__(BT) void epi_bwd_reg(EpiBwdArgs a) {
+  constexpr int U = kU<T>, kGroups = BT / NT;
+  __shared__ uint32_t upart[2][BT / 64];
+  __shared__ float cols[NT == BT ? 1 : NT * V * U];
+  const int t = threadIdx.x & (NT - 1);
+  const int grp = NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  Units<T, NT, V> un;
+  un.init((int32_t)a.C, t);
+  float acc[V][U];
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+#pragma unroll
+    for (int i = 0; i < U; ++i) acc[j][i] = 0.f;
+  int flip = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kGroups + grp; row < a.R; row += (int64_t)gridDim.x * kGroups, flip ^= 1) {
+    const int64_t base = row * a.C;
+    typename Raw<T>::V dy[V], z[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        dy[j] = load_raw(static_cast<const T *>(a.dY) + base + un.off[j]);
+        z[j] = load_raw(static_cast<const T *>(a.Z) + base + un.off[j]);
+      }
+    float d[V][U];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        float f[U];
+        unpack(dy[j], d[j]);
+        unpack(z[j], f);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          d[j][i] = back(d[j][i], f[i], a.act);
+          acc[j][i] += d[j][i];
+          m = umax(m, mag(d[j][i]));
+        }
+      }
+    const float s = __fdiv_rn(row_max<NT>(m, upart[flip]), 127.f), r = __fdiv_rn(1.f, s);
+    const bool fast = fast_scale(s);
+    if (t == 0) a.scale[row] = s;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        store_raw(static_cast<T *>(a.dZ) + base + un.off[j], pack(d[j]));
+        store_q<U>(a.Q + base + un.off[j], d[j], s, r, fast);
+      }
+  }
+  if (a.P) write_cols<T, NT, V, BT>(acc, un, grp, cols, a.P + (int64_t)blockIdx.x * a.C);
 }
 
 template <class T>
@@ -241,24 +693,48 @@ __global__ __launch_bounds__(kNT) void col_sums(const T *__restrict__ A, const T
   P[blockIdx.y * C + c] = sum;
 }
 
-// the strips' sums added in strip order
-__global__ __launch_bounds__(kNT) void col_finish(const float *__restrict__ P, float *__restrict__ out, int64_t strips,
-                                                  int64_t C) {
-  const int64_t c = (int64_t)blockIdx.x * kNT + threadIdx.x;
-  if (c >= C) return;
+// the rows of P added up: a workgroup takes 32 columns, its 32 groups of 32
+// threads each every 32nd row, eight loads at a time, and the groups' sums
+// meet in LDS in order
+constexpr int kFinCols = 32, kFinGroups = 32, kFinT = kFinCols * kFinGroups;
+__global__ __launch_bounds__(kFinT) void col_finish(const float *__restrict__ P, float *__restrict__ out, int64_t rows,
+                                                    int64_t C) {
+  __shared__ float part[kFinGroups][kFinCols + 1];
+  const int c = threadIdx.x % kFinCols, g = threadIdx.x / kFinCols;
+  const int64_t col = (int64_t)blockIdx.x * kFinCols + c;
   float sum = 0.f;
-  for (int64_t s = 0; s < strips; ++s) sum += P[s * C + c];
-  out[c] = sum;
+  if (col < C)
+    for (int64_t r0 = g; r0 < rows; r0 += 8 * kFinGroups) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = r0 + k * kFinGroups < rows ? P[(r0 + k * kFinGroups) * C + col] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum += v[k];
+    }
+  part[g][c] = sum;
+  __syncthreads();
+  if (g == 0 && col < C) {
+#pragma unroll
+    for (int i = 1; i < kFinGroups; ++i) sum += part[i][c];
+    out[col] = sum;
+  }
 }
 
 constexpr int64_t kMaxStrips = 512;
 int64_t strips_of(int64_t R) { return R < kMaxStrips ? R : kMaxStrips; }
 
 // ---------------------------------------------------------------------------
-// Clipping
+// Clipping.  Two launches over the tensors' chunks: the sums of squares, one
+// double a workgroup, then the scaling, whose workgroups each add those
+// doubles up again in one order (a few KB from the caches, in place of a
+// third launch).  A square of any float32 fits a double, so neither end of
+// the range is lost.  The second pass takes the chunks from the last to the
+// first: what the first pass read last is still in the caches (256 MB behind
+// the L2s), and reading it again costs no HBM.
 // ---------------------------------------------------------------------------
-constexpr int kGroup = 64;             // tensors per launch
-constexpr int64_t kChunk = 16384;      // elements per workgroup
+constexpr int kGroup = 96;                 // tensors per launch
+constexpr int kChunk = 8 * kNT * 4;        // elements per workgroup and step, at most
+constexpr int64_t kMaxParts = 1024;        // workgroups of the first pass, over all launches (and one each)
 
 // the tensors of one launch; first[i]: the first chunk of tensor i
 struct Tensors {
@@ -271,56 +747,113 @@ struct Tensors {
 };
 
 __device__ __forceinline__ int tensor_of(const Tensors &ts, int32_t chunk) {
-  int i = 0;
-  while (i + 1 < ts.count && ts.first[i + 1] <= chunk) ++i;
-  return i;
+  int lo = 0, hi = ts.count;   // first[lo] <= chunk < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ts.first[mid] <= chunk)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double block_sum_d(double v, double *part) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// the squares of elements e0 .. e1 of a tensor, 16 bytes a load, four in flight
+template <class T>
+__device__ __forceinline__ double chunk_sumsq(const T *p, int64_t e0, int64_t e1) {
+  constexpr int U = kU<T>;
+  const int n = (int)(e1 - e0), nu = n / U;
+  p += e0;
+  double sum = 0.0;
+  for (int u0 = threadIdx.x; u0 < nu; u0 += 4 * kNT) {
+    typename Raw<T>::V r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (u0 + k * kNT < nu) r[k] = load_raw(p + (u0 + k * kNT) * U);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (u0 + k * kNT < nu) {
+        float v[U];
+        unpack(r[k], v);
+#pragma unroll
+        for (int i = 0; i < U; ++i) sum = __builtin_fma((double)v[i], (double)v[i], sum);
+      }
+  }
+  const int e = nu * U + (int)threadIdx.x;   // at most U - 1 elements past the units
+  if (e < n) {
+    const double v = widen(p[e]);
+    sum = __builtin_fma(v, v, sum);
+  }
+  return sum;
 }
 
 __global__ __launch_bounds__(kNT) void sumsq(Tensors ts, double *__restrict__ part) {
   __shared__ double wsum[4];
-  const int i = tensor_of(ts, blockIdx.x);
-  const int64_t e0 = (int64_t)(blockIdx.x - ts.first[i]) * kChunk;
-  const int64_t e1 = e0 + kChunk < ts.size[i] ? e0 + kChunk : ts.size[i];
   double sum = 0.0;
-  for (int64_t e = e0 + threadIdx.x; e < e1; e += kNT) {
-    const double v = ts.bf16[i] ? widen(static_cast<const uint16_t *>(ts.in[i])[e]) : static_cast<const float *>(ts.in[i])[e];
-    sum = __builtin_fma(v, v, sum);
+  for (int32_t c = blockIdx.x; c < ts.first[ts.count]; c += gridDim.x) {
+    const int i = tensor_of(ts, c);
+    const int64_t e0 = (int64_t)(c - ts.first[i]) * kChunk;
+    const int64_t e1 = e0 + kChunk < ts.size[i] ? e0 + kChunk : ts.size[i];
+    sum += ts.bf16[i] ? chunk_sumsq(static_cast<const uint16_t *>(ts.in[i]), e0, e1)
+                      : chunk_sumsq(static_cast<const float *>(ts.in[i]), e0, e1);
   }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-  if ((threadIdx.x & 63) == 0) wsum[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) part[blockIdx.x] = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
+  sum = block_sum_d(sum, wsum);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-// one workgroup: the partial sums in a fixed order, the norm, the factor
-__global__ __launch_bounds__(kNT) void norm_finish(const double *__restrict__ part, int64_t n, float max_norm, float eps,
-                                                   float *__restrict__ norm, float *__restrict__ factor) {
+template <class T>
+__device__ __forceinline__ void chunk_scale(const T *p, T *q, int64_t e0, int64_t e1, float f) {
+  constexpr int U = kU<T>;
+  const int n = (int)(e1 - e0), nu = n / U;
+  p += e0;
+  q += e0;
+  for (int u0 = threadIdx.x; u0 < nu; u0 += 4 * kNT) {
+    typename Raw<T>::V r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (u0 + k * kNT < nu) r[k] = load_raw(p + (u0 + k * kNT) * U);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (u0 + k * kNT < nu) {
+        float v[U];
+        unpack(r[k], v);
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] *= f;
+        store_raw(q + (u0 + k * kNT) * U, pack(v));
+      }
+  }
+  const int e = nu * U + (int)threadIdx.x;
+  if (e < n) q[e] = narrow<T>(widen(p[e]) * f);
+}
+
+// `parts` doubles from the first pass; workgroup 0 of the first launch writes the norm
+__global__ __launch_bounds__(kNT) void scale_all(Tensors ts, const double *__restrict__ part, int32_t parts,
+                                                 float max_norm, float eps, float *__restrict__ norm) {
   __shared__ double wsum[4];
   double sum = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += kNT) sum += part[i];
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-  if ((threadIdx.x & 63) == 0) wsum[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const float v = (float)__dsqrt_rn((wsum[0] + wsum[1]) + (wsum[2] + wsum[3]));
-    *norm = v;
-    const float f = __fdiv_rn(max_norm, v + eps);
-    *factor = f > 1.f ? 1.f : f;
-  }
-}
-
-__global__ __launch_bounds__(kNT) void scale_all(Tensors ts, const float *__restrict__ factor) {
-  const int i = tensor_of(ts, blockIdx.x);
-  const int64_t e0 = (int64_t)(blockIdx.x - ts.first[i]) * kChunk;
-  const int64_t e1 = e0 + kChunk < ts.size[i] ? e0 + kChunk : ts.size[i];
-  const float f = *factor;
-  for (int64_t e = e0 + threadIdx.x; e < e1; e += kNT) {
+  for (int32_t i = threadIdx.x; i < parts; i += kNT) sum += part[i];
+  const float v = (float)__dsqrt_rn(block_sum_d(sum, wsum));
+  float f = __fdiv_rn(max_norm, v + eps);
+  f = f > 1.f ? 1.f : f;
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+  const int32_t chunks = ts.first[ts.count];
+  for (int32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+    const int32_t c = chunks - 1 - k;
+    const int i = tensor_of(ts, c);
+    const int64_t e0 = (int64_t)(c - ts.first[i]) * kChunk;
+    const int64_t e1 = e0 + kChunk < ts.size[i] ? e0 + kChunk : ts.size[i];
     if (ts.bf16[i])
-      static_cast<uint16_t *>(ts.out[i])[e] = narrow<uint16_t>(widen(static_cast<const uint16_t *>(ts.in[i])[e]) * f);
+      chunk_scale(static_cast<const uint16_t *>(ts.in[i]), static_cast<uint16_t *>(ts.out[i]), e0, e1, f);
     else
-      static_cast<float *>(ts.out[i])[e] = static_cast<const float *>(ts.in[i])[e] * f;
+      chunk_scale(static_cast<const float *>(ts.in[i]), static_cast<float *>(ts.out[i]), e0, e1, f);
   }
 }
 
@@ -382,9 +915,89 @@ bool lists_overlap(const void *const *grads, void *const *outs, const int64_t *s
   return false;
 }
 
+// the tensors g0 .. of a launch, empty ones left out
+void fill(Tensors &ts, const void *const *grads, void *const *outs, const int64_t *sizes, const int32_t *kinds,
+          int64_t g0, int64_t count) {
+  ts.count = 0;
+  ts.first[0] = 0;
+  for (int64_t i = g0; i < count && i < g0 + kGroup; ++i) {
+    if (sizes[i] == 0) continue;
+    const int j = ts.count++;
+    ts.in[j] = grads[i];
+    ts.out[j] = outs[i];
+    ts.size[j] = sizes[i];
+    ts.bf16[j] = kinds[i] == TGEMM_IN_BF16;
+    ts.first[j + 1] = ts.first[j] + (int32_t)ceil_div(sizes[i], kChunk);
+  }
+}
+
 int done() { return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP; }
 
 int64_t col_ws_bytes(int64_t R, int64_t C) { return 4 * strips_of(R) * C; }
+
+void launch_finish(const float *P, float *out, int64_t rows, int64_t C, hipStream_t stream) {
+  hipLaunchKernelGGL(col_finish, dim3((unsigned)ceil_div(C, kFinCols)), dim3(kFinT), 0, stream, P, out, rows, C);
+}
+
+// NT and V of the register kernels, for rows of U to 16384 elements: a wave a
+// row while its lanes hold the row in four units and there are rows for four
+// waves a CU, else a workgroup of 256 or 1024.  nt 0: the looped kernels.
+struct RowPlan {
+  int nt, v, bt;
+  int64_t grid;   // workgroups
+};
+RowPlan row_plan(int64_t R, int64_t C, int U, int64_t waves_per_cu) {
+  RowPlan p = {0, 0, 0, 0};
+  const int64_t nu = ceil_div(C, U);
+  if (C < U || C > 16384) return p;
+  p.nt = nu <= 256 && (R >= 1024 || nu <= 64) ? 64 : nu <= 1024 ? 256 : 1024;
+  p.bt = p.nt == 64 ? 256 : p.nt;
+  p.v = (int)ceil_div(nu, p.nt);
+  const int64_t groups = ceil_div(R, p.bt / p.nt);
+  const int64_t cap = kCUs * (64 * waves_per_cu > p.bt ? 64 * waves_per_cu / p.bt : 1);
+  p.grid = groups < cap ? groups : cap;
+  return p;
+}
+
+// the row kernel K<T, NT, V, BT> of a plan
+#define ROW_CASE(NT, V, BT) \
+  case NT * 8 + V: hipLaunchKernelGGL((Kernel::template Of<T, NT, V, BT>::run), g, b, 0, stream, a); break;
+template <class Kernel, class T>
+void row_launch(const RowPlan &p, const typename Kernel::Args &a, hipStream_t stream) {
+  const dim3 g((unsigned)p.grid), b((unsigned)p.bt);
+  switch (p.nt * 8 + p.v) {
+    ROW_CASE(64, 1, 256) ROW_CASE(64, 2, 256) ROW_CASE(64, 3, 256) ROW_CASE(64, 4, 256)
+    ROW_CASE(256, 1, 256) ROW_CASE(256, 2, 256) ROW_CASE(256, 3, 256) ROW_CASE(256, 4, 256)
+    ROW_CASE(1024, 2, 1024)
+    default: break;
+  }
+  if constexpr (kU<T> == 4) {   // float32 rows past 8192
+    switch (p.nt * 8 + p.v) {
+      ROW_CASE(1024, 3, 1024) ROW_CASE(1024, 4, 1024)
+      default: break;
+    }
+  }
+}
+#undef ROW_CASE
+#define ROW_KERNEL(NAME, KERNEL, ARGS)                                      \
+  struct NAME {                                                             \
+    typedef ARGS Args;                                                      \
+    template <class T, int NT, int V, int BT>                               \
+    struct Of {                                                             \
+      static constexpr auto run = KERNEL<T, NT, V, BT>;                     \
+    };                                                                      \
+  };
+ROW_KERNEL(NormReg, norm_reg, NormArgs)
+ROW_KERNEL(NormBwdReg, norm_bwd_reg, NormBwdArgs)
+ROW_KERNEL(EpiBwdReg, epi_bwd_reg, EpiBwdArgs)
+#undef ROW_KERNEL
+template <class Kernel>
+void row_launch(int kind, const RowPlan &p, const typename Kernel::Args &a, hipStream_t stream) {
+  if (kind == TGEMM_IN_F32)
+    row_launch<Kernel, float>(p, a, stream);
+  else
+    row_launch<Kernel, uint16_t>(p, a, stream);
+}
 
 template <class T, bool NORM>
 void launch_cols(const T *A, const T *B, const float *rstd, int act, float *P, float *out, int64_t R, int64_t C,
@@ -393,7 +1006,7 @@ void launch_cols(const T *A, const T *B, const float *rstd, int act, float *P, f
   const unsigned gx = (unsigned)ceil_div(C, kNT);
   hipLaunchKernelGGL((col_sums<T, NORM>), dim3(gx, (unsigned)strips), dim3(kNT), 0, stream, A, B, rstd, act, P, R, C,
                      strip);
-  hipLaunchKernelGGL(col_finish, dim3(gx), dim3(kNT), 0, stream, P, out, strips, C);
+  launch_finish(P, out, strips, C, stream);
 }
 
 }  // namespace
@@ -413,6 +1026,11 @@ int ternary_rmsnorm_quantize(const void *X, int in_kind, const void *residual, c
   const void *const same[5][2] = {{X, residual}};
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
   const NormArgs a = {X, residual, gain, H, Y, rstd, scale, Q, eps, R, C};
+  const RowPlan p = row_plan(R, C, in_kind == TGEMM_IN_F32 ? 4 : 8, kNormWaves);
+  if (p.nt) {
+    row_launch<NormReg>(in_kind, p, a, stream);
+    return done();
+  }
   const dim3 g((unsigned)(R < kMaxRowGrid ? R : kMaxRowGrid));
   if (in_kind == TGEMM_IN_F32)
     hipLaunchKernelGGL(norm_rows<float>, g, dim3(kNT), 0, stream, a);
@@ -442,9 +1060,16 @@ int ternary_rmsnorm_backward(const void *dY, const void *H, int in_kind, const f
   const Buf ins[] = {{dY, xb}, {H, xb}, {gain, 4 * C}, {rstd, 4 * R}, {dH, xb}};
   const void *const same[3][2] = {{dH, dH}};
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
-  const NormBwdArgs a = {dY, H, gain, rstd, dH, dX, R, C};
-  const dim3 g((unsigned)(R < kMaxRowGrid ? R : kMaxRowGrid));
   float *P = static_cast<float *>(workspace);
+  NormBwdArgs a = {dY, H, gain, rstd, dH, dX, P, R, C};
+  const RowPlan p = row_plan(R, C, in_kind == TGEMM_IN_F32 ? 4 : 8, kBwdWaves);
+  if (p.nt) {
+    if (p.grid == 1) a.P = dgain;
+    row_launch<NormBwdReg>(in_kind, p, a, stream);
+    if (p.grid > 1) launch_finish(P, dgain, p.grid, C, stream);
+    return done();
+  }
+  const dim3 g((unsigned)(R < kMaxRowGrid ? R : kMaxRowGrid));
   if (in_kind == TGEMM_IN_F32) {
     hipLaunchKernelGGL(norm_bwd_rows<float>, g, dim3(kNT), 0, stream, a);
     launch_cols<float, true>(static_cast<const float *>(dY), static_cast<const float *>(H), rstd, 0, P, dgain, R, C,
@@ -475,9 +1100,16 @@ int ternary_epilogue_backward(const void *dY, const void *Z, int in_kind, int ac
   const Buf ins[] = {{dY, xb}, {Z, xb}};
   const void *const same[5][2] = {};
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
-  const EpiBwdArgs a = {dY, Z, dZ, Q, scale, R, C, act};
-  const dim3 g((unsigned)(R < kMaxRowGrid ? R : kMaxRowGrid));
   float *P = static_cast<float *>(workspace);
+  EpiBwdArgs a = {dY, Z, dZ, Q, scale, dbias ? P : nullptr, R, C, act};
+  const RowPlan p = row_plan(R, C, in_kind == TGEMM_IN_F32 ? 4 : 8, kBwdWaves);
+  if (p.nt) {
+    if (p.grid == 1) a.P = dbias;
+    row_launch<EpiBwdReg>(in_kind, p, a, stream);
+    if (dbias && p.grid > 1) launch_finish(P, dbias, p.grid, C, stream);
+    return done();
+  }
+  const dim3 g((unsigned)(R < kMaxRowGrid ? R : kMaxRowGrid));
   if (in_kind == TGEMM_IN_F32) {
     hipLaunchKernelGGL(epi_bwd_rows<float>, g, dim3(kNT), 0, stream, a);
     if (dbias)
@@ -501,7 +1133,8 @@ int ternary_clip_grad_norm_workspace(const int64_t *sizes, int64_t count, int64_
     chunks += ceil_div(sizes[i], kChunk);
     if (chunks > INT32_MAX) return TGEMM_ERR_DIM;
   }
-  *bytes = 16 + 8 * chunks;
+  const int64_t launches = ceil_div(count, kGroup);
+  *bytes = 8 * ((chunks < kMaxParts ? chunks : kMaxParts) + launches + 1);
   return TGEMM_OK;
 }
 
@@ -531,34 +1164,29 @@ int ternary_clip_grad_norm(const void *const *grads, void *const *outs, const in
     return TGEMM_ERR_DIM;   // more gradients than the host can list
   }
   if (overlap(norm, 4, workspace, need)) return TGEMM_ERR_ALIAS;
-  float *factor = static_cast<float *>(workspace);
-  double *part = reinterpret_cast<double *>(static_cast<char *>(workspace) + 16);
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t done_chunks = 0;
-    Tensors ts;
-    ts.count = 0;
-    ts.first[0] = 0;
-    for (int64_t i = 0; i < count; ++i) {
-      if (sizes[i] > 0) {
-        const int j = ts.count++;
-        ts.in[j] = grads[i];
-        ts.out[j] = outs[i];
-        ts.size[j] = sizes[i];
-        ts.bf16[j] = kinds[i] == TGEMM_IN_BF16;
-        ts.first[j + 1] = ts.first[j] + (int32_t)ceil_div(sizes[i], kChunk);
-      }
-      const int32_t chunks = ts.first[ts.count];
-      if (chunks > 0 && (ts.count == kGroup || i == count - 1)) {
-        if (pass == 0)
-          hipLaunchKernelGGL(sumsq, dim3((unsigned)chunks), dim3(kNT), 0, stream, ts, part + done_chunks);
-        else
-          hipLaunchKernelGGL(scale_all, dim3((unsigned)chunks), dim3(kNT), 0, stream, ts, factor);
-        done_chunks += chunks;
-        ts.count = 0;
-      }
-    }
-    if (pass == 0)
-      hipLaunchKernelGGL(norm_finish, dim3(1), dim3(kNT), 0, stream, part, done_chunks, max_norm, eps, norm, factor);
+  double *part = static_cast<double *>(workspace);
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) total += ceil_div(sizes[i], kChunk);
+  // the first pass forwards, the second backwards over the launches too
+  int64_t parts = 0;
+  Tensors ts;
+  for (int64_t g0 = 0; g0 < count; g0 += kGroup) {
+    fill(ts, grads, outs, sizes, kinds, g0, count);
+    const int64_t chunks = ts.first[ts.count], share = kMaxParts * chunks / (total ? total : 1);
+    if (chunks == 0) continue;
+    const int64_t grid = chunks < kMaxParts && total <= kMaxParts ? chunks : share > 1 ? share : 1;
+    hipLaunchKernelGGL(sumsq, dim3((unsigned)grid), dim3(kNT), 0, stream, ts, part + parts);
+    parts += grid;
+  }
+  bool first = true;
+  for (int64_t g0 = (count - 1) / kGroup * kGroup; g0 >= 0; g0 -= kGroup) {
+    if (count > kGroup || total == 0) fill(ts, grads, outs, sizes, kinds, g0, count);
+    const int64_t chunks = ts.first[ts.count];
+    if (chunks == 0 && !(first && g0 == 0)) continue;
+    const int64_t cap = kCUs * 8, grid = chunks < 1 ? 1 : chunks < cap ? chunks : cap;
+    hipLaunchKernelGGL(scale_all, dim3((unsigned)grid), dim3(kNT), 0, stream, ts, part, (int32_t)parts, max_norm, eps,
+                       first ? norm : nullptr);
+    first = false;
   }
   return done();
 }
