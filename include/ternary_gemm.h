@@ -272,8 +272,9 @@ int ternary_quantize_cols(const void *X, int in_kind, int8_t *Q, float *scale, i
  *     row that holds an infinity or a NaN has it as its scale;
  *   - a call that needs a workspace takes caller-owned DEVICE memory, 16-byte
  *     aligned, of at least the bytes that the query beside it gives
- *     (TGEMM_ERR_WORKSPACE otherwise).  Its contents on entry do not matter;
- *     it is in use until the call completes on `stream`;
+ *     (TGEMM_ERR_WORKSPACE otherwise; where that is 0, NULL will do).  Its
+ *     contents on entry do not matter; it is in use until the call completes
+ *     on `stream`;
  *   - outputs overlap neither inputs nor each other nor the workspace
  *     (TGEMM_ERR_ALIAS), but for the in-place forms named below, where the
  *     two pointers are equal.

@@ -203,9 +203,15 @@ def tile_of(pl: TgemmPlan, workgroup: int, iteration: int = 0):
 # torch-tensor wrappers (same names as the C entry points)
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _check(t, dtype, ndim, what):
@@ -514,13 +520,21 @@ def ternary_quantize_cols(X, Q=None, scale=None, stream=None):
 def _kind(t, what):
     """The kind of a float matrix (IN_* and OUT_* have the same values)."""
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"{what} must be a float32 or bfloat16 torch.Tensor")
-    return IN_F32 if t.dtype == torch.float32 else IN_BF16
+    if isinstance(t, torch.Tensor):
+        if t.dtype == torch.float32:
+            return IN_F32
+        if t.dtype == torch.bfloat16:
+            return IN_BF16
+    raise TypeError(f"{what} must be a float32 or bfloat16 torch.Tensor")
 
 
 def _given(t, dtype, shape, device, what):
-    """An argument that has to have this type, shape and device."""
+    """An argument that has to have this type, shape and device (a GPU's)."""
+    try:
+        if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t
+    except AttributeError:   # not a tensor: _check says so
+        pass
     _check(t, dtype, len(shape), what)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
@@ -542,15 +556,33 @@ def _made(t, dtype, shape, device, what, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _like(t, x, stream, what):
+    """The caller's output of x's type and shape, or a new one."""
+    if t is None and stream is None:
+        return _torch().empty_like(x)
+    return _made(t, x.dtype, x.shape, x.device, what, stream)
+
+
 def _scratch(workspace, nbytes, device, stream):
-    """The caller's workspace (a contiguous uint8 device tensor), or a new one."""
+    """The caller's workspace (a contiguous uint8 device tensor), or a new one;
+    None if the call needs none."""
     torch = _torch()
     if workspace is None:
-        return _made(None, torch.uint8, (nbytes,), device, "workspace", stream)
+        return _made(None, torch.uint8, (nbytes,), device, "workspace", stream) if nbytes else None
     _check(workspace, torch.uint8, 1, "workspace")
     if workspace.device != device:
         raise ValueError(f"workspace must be on {device}, got {workspace.device}")
     return workspace
+
+
+def _raw_stream(stream, device):
+    """The handle of `stream`, or of the device's current one (the direct
+    query where this torch has it: making a Stream object takes 2 us)."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    query = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(device).cuda_stream if query is None else query(device.index)
 
 
 def _ptr(t):
@@ -589,21 +621,21 @@ def ternary_rmsnorm_quantize(X, gain, eps=1e-6, residual=None, save=False, H=Non
     (R, C), dt, dev = X.shape, X.dtype, X.device
     _given(gain, torch.float32, (C,), dev, "gain")
     if residual is not None:
-        _given(residual, dt, (R, C), dev, "residual")
-        H = _made(H, dt, (R, C), dev, "H", stream)
+        _given(residual, dt, X.shape, dev, "residual")
+        H = _like(H, X, stream, "H")
     elif H is not None and H is not X:
         raise ValueError("H is given without a residual: it would be X")
     if not save and (Y is not None or rstd is not None):
         raise ValueError("Y and rstd are outputs of save=True")
     if save:
-        Y = _made(Y, dt, (R, C), dev, "Y", stream)
+        Y = _like(Y, X, stream, "Y")
         rstd = _made(rstd, torch.float32, (R,), dev, "rstd", stream)
     Q = _made(Q, torch.int8, (R, C), dev, "Q", stream)
     scale = _made(scale, torch.float32, (R,), dev, "scale", stream)
     _done("ternary_rmsnorm_quantize",
           lib().ternary_rmsnorm_quantize(X.data_ptr(), kind, _ptr(residual), gain.data_ptr(), eps,
                                          None if residual is None else H.data_ptr(), _ptr(Y), _ptr(rstd),
-                                         Q.data_ptr(), scale.data_ptr(), R, C, _stream(stream, dev)))
+                                         Q.data_ptr(), scale.data_ptr(), R, C, _raw_stream(stream, dev)))
     return Q, scale, X if residual is None else H, Y, rstd
 
 
@@ -620,13 +652,13 @@ def ternary_rmsnorm_backward(dY, H, gain, rstd, dH=None, dX=None, dgain=None, wo
     _given(rstd, torch.float32, (R,), dev, "rstd")
     if dH is not None:
         _given(dH, dt, (R, C), dev, "dH")
-    dX = _made(dX, dt, (R, C), dev, "dX", stream)
+    dX = _like(dX, H, stream, "dX")
     dgain = _made(dgain, torch.float32, (C,), dev, "dgain", stream)
     ws = _scratch(workspace, _queried("ternary_rmsnorm_backward_workspace", R, C), dev, stream)
     _done("ternary_rmsnorm_backward",
           lib().ternary_rmsnorm_backward(dY.data_ptr(), H.data_ptr(), kind, gain.data_ptr(), rstd.data_ptr(),
-                                         _ptr(dH), dX.data_ptr(), dgain.data_ptr(), R, C, ws.data_ptr(), ws.numel(),
-                                         _stream(stream, dev)))
+                                         _ptr(dH), dX.data_ptr(), dgain.data_ptr(), R, C, _ptr(ws),
+                                         0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
     return dX, dgain
 
 
@@ -659,7 +691,7 @@ def ternary_gemm_s8_epilogue(A, Wpacked, a_row_scale, w_scale, bias=None, act="n
     _done("ternary_gemm_s8_epilogue",
           lib().ternary_gemm_s8_epilogue(A.data_ptr(), Wpacked.data_ptr(), a_row_scale.data_ptr(), float(w_scale),
                                          _ptr(bias), act, _ptr(residual), Y.data_ptr(), _ptr(Z), kind, M, N, K,
-                                         _stream(stream, dev)))
+                                         _raw_stream(stream, dev)))
     return Y, Z
 
 
@@ -674,7 +706,7 @@ def ternary_epilogue_backward(dY, Z, act="none", bias=True, dZ=None, dbias=None,
     (R, C), dt, dev = Z.shape, Z.dtype, Z.device
     _given(dY, dt, (R, C), dev, "dY")
     act = _act(act)
-    dZ = _made(dZ, dt, (R, C), dev, "dZ", stream)
+    dZ = _like(dZ, Z, stream, "dZ")
     ws = None
     if bias:
         dbias = _made(dbias, torch.float32, (C,), dev, "dbias", stream)
@@ -686,7 +718,7 @@ def ternary_epilogue_backward(dY, Z, act="none", bias=True, dZ=None, dbias=None,
     _done("ternary_epilogue_backward",
           lib().ternary_epilogue_backward(dY.data_ptr(), Z.data_ptr(), kind, act, dZ.data_ptr(), _ptr(dbias),
                                           Q.data_ptr(), scale.data_ptr(), R, C, _ptr(ws),
-                                          0 if ws is None else ws.numel(), _stream(stream, dev)))
+                                          0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
     return dZ, dbias, Q, scale
 
 
@@ -699,25 +731,26 @@ def ternary_clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None, works
     grads = list(grads)
     if not grads:
         raise ValueError("grads must hold at least one tensor")
-    n, dev = len(grads), grads[0].device if isinstance(grads[0], torch.Tensor) else None
-    sizes, kinds = (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
-    src, dst = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)()
+    n = len(grads)
+    kinds = [_kind(g, "every gradient") for g in grads]
+    dev = grads[0].device
     for i, g in enumerate(grads):
-        kinds[i] = _kind(g, f"grads[{i}]")
-        if not g.is_cuda or g.device != dev or not g.is_contiguous():
+        if not (g.is_cuda and g.device == dev and g.is_contiguous()):
             raise ValueError(f"grads[{i}] must be a contiguous tensor on the device of grads[0]")
-        sizes[i], src[i] = g.numel(), g.data_ptr()
     if out is None:
-        out = [_made(None, g.dtype, tuple(g.shape), dev, "out", stream) for g in grads]
-    elif len(out) != n:
-        raise ValueError(f"out must hold {n} tensors, got {len(out)}")
-    for i, (g, o) in enumerate(zip(grads, out)):
-        if o is not g:
-            _given(o, g.dtype, tuple(g.shape), dev, f"out[{i}]")
-        dst[i] = o.data_ptr()
+        out = [_like(None, g, stream, "out") for g in grads]
+    else:
+        if len(out) != n:
+            raise ValueError(f"out must hold {n} tensors, got {len(out)}")
+        if out is not grads:
+            for i, g in enumerate(grads):
+                _given(out[i], g.dtype, g.shape, dev, f"out[{i}]")
+    p = ctypes.c_void_p * n
+    src, dst = p(*[g.data_ptr() for g in grads]), p(*[o.data_ptr() for o in out])
+    sizes, kinds = (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int32 * n)(*kinds)
     norm = _made(norm, torch.float32, (1,), dev, "norm", stream)
     ws = _scratch(workspace, _queried("ternary_clip_grad_norm_workspace", sizes, n), dev, stream)
     _done("ternary_clip_grad_norm",
           lib().ternary_clip_grad_norm(src, dst, sizes, kinds, n, max_norm, eps, norm.data_ptr(), ws.data_ptr(),
-                                       ws.numel(), _stream(stream, dev)))
+                                       ws.numel(), _raw_stream(stream, dev)))
     return out, norm

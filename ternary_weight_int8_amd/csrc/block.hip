@@ -34,7 +34,7 @@ constexpr int64_t kNormWaves = 32, kBwdWaves = 8;    // waves a CU of the row ke
 
 bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a && b && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+  return a && b && an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
 }
 bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -87,16 +87,17 @@ __device__ __forceinline__ float block_max(uint32_t v, uint32_t *part) {
 // over a row before they can write it, so a row is read once into registers,
 // reduced, and written from them: HBM sees every input and output once.
 //
-// NT threads share a row (a wave, four waves or sixteen), each holding V units
-// of 16 bytes (U elements): unit j of thread t is unit t + NT j of the row, so
-// a wave's loads cover whole lines.  Rows need not be whole units or aligned:
+// A wave (W = 1, several rows a workgroup) or a workgroup of 1 to 16 waves (W = 0)
+// takes a row, each of its NT threads holding V units of 16 bytes (U elements):
+// unit j of thread t is unit t + NT j of the row, so a wave's loads cover whole
+// lines.  Rows need not be whole units or aligned:
 // loads and stores are element-aligned vectors (gfx950 serves them), and the
 // row's last unit is the last U elements, of which the first `dup` also
 // belong to the unit before; both threads compute and store the same values
 // for them, and only the row's sums and the column sums leave them out.  (A
 // store never precedes the reduction that every load of the row precedes, so
 // this holds for in-place outputs too.)  Rows of fewer than U elements, and
-// rows that no NT, V holds, take the looped kernels further down.
+// rows that no W, V holds, take the looped kernels further down.
 // ---------------------------------------------------------------------------
 template <class T>
 constexpr int kU = 16 / (int)sizeof(T);
@@ -165,37 +166,44 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   const uint32_t c = __builtin_amdgcn_readlane((int)v, 32), d = __builtin_amdgcn_readlane((int)v, 48);
   return umax(umax(a, b), umax(c, d));
 }
-// over the NT threads of a row: a wave by itself, or the workgroup's NT / 64
-// waves through `part` (one word a wave).  One barrier: a caller alternates
-// between two `part`s from row to row, and the barrier of the row between
-// separates the reads of one from the next writes to it.
-template <int NT>
+// over a row's threads: a wave by itself, or the workgroup's waves through
+// `part` (a word a wave), which every sixteen lanes then reduce.  One barrier:
+// a caller alternates between two `part`s from row to row, and the barrier of
+// the row between separates the reads of one from the next writes to it.
+template <int W>
 __device__ __forceinline__ float row_sum(float v, float *part) {
   v = wave_sum(v);
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  if constexpr (W == 0) {
+    const int lane = threadIdx.x & 63, l = lane & 15;
+    if (lane == 0) part[threadIdx.x >> 6] = v;
     lds_barrier();
-    v = part[0];
-#pragma unroll
-    for (int i = 1; i < NT / 64; ++i) v += part[i];
+    v = l < (int)(blockDim.x >> 6) ? part[l] : 0.f;
+    v += __uint_as_float(dpp<kXor1>(__float_as_uint(v)));
+    v += __uint_as_float(dpp<kXor2>(__float_as_uint(v)));
+    v += __uint_as_float(dpp<kHalfMirror>(__float_as_uint(v)));
+    v += __uint_as_float(dpp<kMirror>(__float_as_uint(v)));
   }
   return v;
 }
-template <int NT>
+template <int W>
 __device__ __forceinline__ float row_max(uint32_t v, uint32_t *part) {
   v = wave_max(v);
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  if constexpr (W == 0) {
+    const int lane = threadIdx.x & 63, l = lane & 15;
+    if (lane == 0) part[threadIdx.x >> 6] = v;
     lds_barrier();
-    v = part[0];
-#pragma unroll
-    for (int i = 1; i < NT / 64; ++i) v = umax(v, part[i]);
+    v = l < (int)(blockDim.x >> 6) ? part[l] : 0u;
+    v = umax(v, dpp<kXor1>(v));
+    v = umax(v, dpp<kXor2>(v));
+    v = umax(v, dpp<kHalfMirror>(v));
+    v = umax(v, dpp<kMirror>(v));
   }
   return __uint_as_float(v);
 }
+constexpr int max_t(int W, int V) { return W && V > 1 ? 256 : 1024; }   // threads a workgroup, at most
 
 // A thread's units of a row of C elements
-template <class T, int NT, int V>
+template <class T, int W, int V>
 struct Units {
   static constexpr int U = kU<T>;
   int off[V];    // first element of each unit
@@ -203,6 +211,7 @@ struct Units {
   int32_t last;  // j of the thread's unit if that is the row's last and dup > 0, else -1
   int32_t n;     // units of the thread
   __device__ __forceinline__ void init(int32_t C, int t) {
+    const int32_t NT = W ? 64 : (int32_t)blockDim.x;
     const int32_t nu = (C + U - 1) / U;
     dup = nu * U - C;
     last = dup && (nu - 1) % NT == t ? (nu - 1) / NT : -1;
@@ -334,25 +343,24 @@ __global__ __launch_bounds__(kNT) void norm_rows(NormArgs a) {
   }
 }
 
-// rows in registers, grid-stride over groups of NT threads; the gain stays in
+// rows in registers, grid-stride over them; the gain stays in
 // registers from row to row
-template <class T, int NT, int V, int BT>
-__global__ __launch_bounds__(BT) void norm_reg(NormArgs a) {
+template <class T, int W, int V>
+__global__ __launch_bounds__(max_t(W, V)) void norm_reg(NormArgs a) {
   constexpr int U = kU<T>;
-  __shared__ float part[2][BT / 64];
-  __shared__ uint32_t upart[2][BT / 64];
-  const int t = threadIdx.x & (NT - 1);
-  const int grp = NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
-  constexpr int kGroups = BT / NT;
-  static_assert(NT == 64 || NT == BT, "a wave or the workgroup");
-  Units<T, NT, V> un;
+  __shared__ float part[2][16];
+  __shared__ uint32_t upart[2][16];
+  const int t = W ? threadIdx.x & 63 : threadIdx.x;
+  const int grp = W ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  Units<T, W, V> un;
   un.init((int32_t)a.C, t);
   float gain[V][U];
 #pragma unroll
   for (int j = 0; j < V; ++j)
     if (un.on(j)) load_f<U>(a.gain + un.off[j], gain[j]);
   int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kGroups + grp; row < a.R; row += (int64_t)gridDim.x * kGroups, flip ^= 1) {
+  const int groups = W ? (int)(blockDim.x >> 6) : 1;
+  for (int64_t row = (int64_t)blockIdx.x * groups + grp; row < a.R; row += (int64_t)gridDim.x * groups, flip ^= 1) {
     const int64_t base = row * a.C;
     const T *x = static_cast<const T *>(a.X) + base;
     typename Raw<T>::V h[V];
@@ -389,7 +397,7 @@ __global__ __launch_bounds__(BT) void norm_reg(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < U; ++i) ss = __builtin_fmaf(f[i], f[i], ss);
       }
-    ss = row_sum<NT>(ss, part[flip]);
+    ss = row_sum<W>(ss, part[flip]);
     const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ss, (float)a.C) + a.eps));
     if (a.res) {
       T *H = static_cast<T *>(a.H) + base;
@@ -409,7 +417,7 @@ __global__ __launch_bounds__(BT) void norm_reg(NormArgs a) {
           m = umax(m, mag(y[j][i]));
         }
       }
-    const float s = __fdiv_rn(row_max<NT>(m, upart[flip]), 127.f), r = __fdiv_rn(1.f, s);
+    const float s = __fdiv_rn(row_max<W>(m, upart[flip]), 127.f), r = __fdiv_rn(1.f, s);
     const bool fast = fast_scale(s);
     if (t == 0) {
       a.scale[row] = s;
@@ -434,8 +442,8 @@ __global__ __launch_bounds__(BT) void norm_reg(NormArgs a) {
 // takes; the sums of a workgroup's groups meet in LDS, and its row of P goes
 // to col_finish, which adds the workgroups up in order.
 // ---------------------------------------------------------------------------
-template <class T, int NT, int V, int BT>
-__device__ __forceinline__ void write_cols(float (&acc)[V][kU<T>], const Units<T, NT, V> &un, int grp, float *lds,
+template <class T, int W, int V>
+__device__ __forceinline__ void write_cols(float (&acc)[V][kU<T>], const Units<T, W, V> &un, int grp, float *lds,
                                            float *__restrict__ P) {
   constexpr int U = kU<T>;
   auto each = [&](auto f) {
@@ -447,15 +455,18 @@ __device__ __forceinline__ void write_cols(float (&acc)[V][kU<T>], const Units<T
           if (j != un.last || i >= un.dup) f(un.off[j] + i, acc[j][i]);
       }
   };
-  if constexpr (NT == BT) {
+  if constexpr (W == 0) {
     each([&](int c, float v) { P[c] = v; });
   } else {
     // group after group adds into LDS
-    for (int g = 0; g < BT / NT; ++g) {
+    const int groups = (int)(blockDim.x >> 6);
+    for (int g = 0; g < groups; ++g) {
       if (grp == g) {
-        if (g == 0)
+        if (groups == 1)
+          each([&](int c, float v) { P[c] = v; });
+        else if (g == 0)
           each([&](int c, float v) { lds[c] = v; });
-        else if (g < BT / NT - 1)
+        else if (g < groups - 1)
           each([&](int c, float v) { lds[c] += v; });
         else
           each([&](int c, float v) { P[c] = lds[c] + v; });
@@ -474,14 +485,14 @@ struct NormBwdArgs {
   int64_t R, C;
 };
 
-template <class T, int NT, int V, int BT>
-__global__ __launch_bounds__(BT) void norm_bwd_reg(NormBwdArgs a) {
-  constexpr int U = kU<T>, kGroups = BT / NT;
-  __shared__ float part[2][BT / 64];
-  __shared__ float cols[NT == BT ? 1 : NT * V * U];
-  const int t = threadIdx.x & (NT - 1);
-  const int grp = NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
-  Units<T, NT, V> un;
+template <class T, int W, int V>
+__global__ __launch_bounds__(max_t(W, V)) void norm_bwd_reg(NormBwdArgs a) {
+  constexpr int U = kU<T>;
+  __shared__ float part[2][16];
+  __shared__ float cols[W ? 64 * V * U : 1];
+  const int t = W ? threadIdx.x & 63 : threadIdx.x;
+  const int grp = W ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  Units<T, W, V> un;
   un.init((int32_t)a.C, t);
   float gain[V][U], acc[V][U];
 #pragma unroll
@@ -492,7 +503,8 @@ __global__ __launch_bounds__(BT) void norm_bwd_reg(NormBwdArgs a) {
   }
   const float invC = __fdiv_rn(1.f, (float)a.C);
   int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kGroups + grp; row < a.R; row += (int64_t)gridDim.x * kGroups, flip ^= 1) {
+  const int groups = W ? (int)(blockDim.x >> 6) : 1;
+  for (int64_t row = (int64_t)blockIdx.x * groups + grp; row < a.R; row += (int64_t)gridDim.x * groups, flip ^= 1) {
     const int64_t base = row * a.C;
     typename Raw<T>::V dy[V], h[V], dh[V];
 #pragma unroll
@@ -522,14 +534,14 @@ __global__ __launch_bounds__(BT) void norm_bwd_reg(NormBwdArgs a) {
         }
         sum += part_sum;
       }
-    if (NT > 64 && a.dH) {
+    if (W == 0 && a.dH) {
       // dX may be dH itself, and two waves may share a row's last elements:
       // dH is in registers before the barrier that the stores come after
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (un.on(j)) asm volatile("" : "+v"(dh[j]));
     }
-    const float mean = row_sum<NT>(sum, part[flip]) * invC;
+    const float mean = row_sum<W>(sum, part[flip]) * invC;
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (un.on(j)) {
@@ -546,7 +558,7 @@ __global__ __launch_bounds__(BT) void norm_bwd_reg(NormBwdArgs a) {
         store_raw(static_cast<T *>(a.dX) + base + un.off[j], pack(d));
       }
   }
-  write_cols<T, NT, V, BT>(acc, un, grp, cols, a.P + (int64_t)blockIdx.x * a.C);
+  write_cols<T, W, V>(acc, un, grp, cols, a.P + (int64_t)blockIdx.x * a.C);
 }
 
 template <class T>
@@ -584,39 +596,59 @@ constexpr float kGeluA = 1.5957691216057308f;              // 2 sqrt(2 / pi)
 constexpr float kGeluAB = 1.5957691216057308f * 0.044715f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// dy * act'(z).  relu2's 2 z is taken as (2 dy) z, which stays finite where
-// the product does.  For z sigmoid(u): p + z p (1 - p) u', p = sigmoid(u) = 1 / (1 + e),
-// 1 - p = e p with e = exp(-u).  Past +-88 the slope is 0 or 1 in single
-// precision (the terms are below 1e-36); the clamp keeps e finite.  It is
-// written with comparisons, which keep a NaN.
-__device__ __forceinline__ float back(float dy, float z, int act) {
-  if (act == TGEMM_ACT_NONE) return dy;
-  if (act == TGEMM_ACT_RELU) return dy * (z > 0.f ? 1.f : (z == z ? 0.f : z));
-  if (act == TGEMM_ACT_RELU2) return (dy + dy) * (z < 0.f ? 0.f : z);
-  const bool silu = act == TGEMM_ACT_SILU;
-  const float c = z < -88.f ? -88.f : (z > 88.f ? 88.f : z), c2 = c * c;
-  const float u = silu ? c : c * (kGeluA + kGeluAB * c2), du = silu ? 1.f : kGeluA + 3.f * kGeluAB * c2;
-  const float e = __builtin_amdgcn_exp2f(fminf(-u * kLog2e, 126.f));
+// dz = dy * act'(z).  For z sigmoid(u) the slope is p + z p (1 - p) u', p =
+// sigmoid(u); silu and gelu differ in four constants and a clamp: with c = z
+// held to +-lim,
+//     t = c (k0 + k1 c^2),  e = 2^t,  p = 1 / (1 + e),  q = e p = 1 - p
+//     act' = p + c (d0 + d1 c^2) q p
+// lim (87 for silu, 10 for gelu) is where the slope reaches 0 or 1 to within
+// 1e-35 and e is still finite.
+struct Sigm {
+  float lim, k0, k1, d0, d1;
+};
+__device__ __forceinline__ Sigm sigm_of(int act) {
+  if (act == TGEMM_ACT_SILU) return {87.f, -kLog2e, 0.f, 1.f, 0.f};
+  return {10.f, -kGeluA * kLog2e, -kGeluAB * kLog2e, kGeluA, 3.f * kGeluAB};
+}
+__device__ __forceinline__ float back_sigm(float dy, float z, const Sigm &k) {
+  const float c = fminf(fmaxf(z, -k.lim), k.lim), c2 = c * c;
+  const float e = __builtin_amdgcn_exp2f(c * __builtin_fmaf(k.k1, c2, k.k0));
   const float p = __builtin_amdgcn_rcpf(1.f + e);
-  return dy * (p + c * p * (e * p) * du);
+  const float w = c * __builtin_fmaf(k.d1, c2, k.d0) * (e * p);
+  const float d = dy * __builtin_fmaf(w, p, p);
+  return z == z ? d : z;   // the clamp drops a NaN
 }
 
-template <class T, int NT, int V, int BT>
-__global__ __launch_bounds__(BT) void epi_bwd_reg(EpiBwdArgs a) {
-  constexpr int U = kU<T>, kGroups = BT / NT;
-  __shared__ uint32_t upart[2][BT / 64];
-  __shared__ float cols[NT == BT ? 1 : NT * V * U];
-  const int t = threadIdx.x & (NT - 1);
-  const int grp = NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
-  Units<T, NT, V> un;
+// relu2's 2 z is taken as (2 dy) z, which stays finite where the product does
+__device__ __forceinline__ float back_relu(float dy, float z) { return dy * (z > 0.f ? 1.f : (z == z ? 0.f : z)); }
+__device__ __forceinline__ float back_relu2(float dy, float z) { return (dy + dy) * (z < 0.f ? 0.f : z); }
+__host__ __device__ __forceinline__ bool is_sigm(int act) { return act >= TGEMM_ACT_SILU; }
+static_assert(TGEMM_ACT_GELU_TANH > TGEMM_ACT_SILU && TGEMM_ACT_RELU2 < TGEMM_ACT_SILU, "is_sigm");
+
+__device__ __forceinline__ float back(float dy, float z, int act) {
+  if (is_sigm(act)) return back_sigm(dy, z, sigm_of(act));
+  return act == TGEMM_ACT_NONE ? dy : act == TGEMM_ACT_RELU ? back_relu(dy, z) : back_relu2(dy, z);
+}
+
+// S: silu and gelu_tanh, else the other three, one uniform branch a unit
+template <class T, int W, int V, int S>
+__global__ __launch_bounds__(max_t(W, V)) void epi_bwd_reg(EpiBwdArgs a) {
+  constexpr int U = kU<T>;
+  __shared__ uint32_t upart[2][16];
+  __shared__ float cols[W ? 64 * V * U : 1];
+  const int t = W ? threadIdx.x & 63 : threadIdx.x;
+  const int grp = W ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  Units<T, W, V> un;
   un.init((int32_t)a.C, t);
   float acc[V][U];
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
     for (int i = 0; i < U; ++i) acc[j][i] = 0.f;
+  const Sigm sg = sigm_of(a.act);
   int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kGroups + grp; row < a.R; row += (int64_t)gridDim.x * kGroups, flip ^= 1) {
+  const int groups = W ? (int)(blockDim.x >> 6) : 1;
+  for (int64_t row = (int64_t)blockIdx.x * groups + grp; row < a.R; row += (int64_t)gridDim.x * groups, flip ^= 1) {
     const int64_t base = row * a.C;
     typename Raw<T>::V dy[V], z[V];
 #pragma unroll
@@ -633,14 +665,23 @@ __global__ __launch_bounds__(BT) void epi_bwd_reg(EpiBwdArgs a) {
         float f[U];
         unpack(dy[j], d[j]);
         unpack(z[j], f);
+        if constexpr (S) {
+#pragma unroll
+          for (int i = 0; i < U; ++i) d[j][i] = back_sigm(d[j][i], f[i], sg);
+        } else if (a.act == TGEMM_ACT_RELU) {
+#pragma unroll
+          for (int i = 0; i < U; ++i) d[j][i] = back_relu(d[j][i], f[i]);
+        } else if (a.act == TGEMM_ACT_RELU2) {
+#pragma unroll
+          for (int i = 0; i < U; ++i) d[j][i] = back_relu2(d[j][i], f[i]);
+        }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          d[j][i] = back(d[j][i], f[i], a.act);
           acc[j][i] += d[j][i];
           m = umax(m, mag(d[j][i]));
         }
       }
-    const float s = __fdiv_rn(row_max<NT>(m, upart[flip]), 127.f), r = __fdiv_rn(1.f, s);
+    const float s = __fdiv_rn(row_max<W>(m, upart[flip]), 127.f), r = __fdiv_rn(1.f, s);
     const bool fast = fast_scale(s);
     if (t == 0) a.scale[row] = s;
 #pragma unroll
@@ -650,7 +691,7 @@ __global__ __launch_bounds__(BT) void epi_bwd_reg(EpiBwdArgs a) {
         store_q<U>(a.Q + base + un.off[j], d[j], s, r, fast);
       }
   }
-  if (a.P) write_cols<T, NT, V, BT>(acc, un, grp, cols, a.P + (int64_t)blockIdx.x * a.C);
+  if (a.P) write_cols<T, W, V>(acc, un, grp, cols, a.P + (int64_t)blockIdx.x * a.C);
 }
 
 template <class T>
@@ -933,63 +974,68 @@ void fill(Tensors &ts, const void *const *grads, void *const *outs, const int64_
 
 int done() { return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP; }
 
-int64_t col_ws_bytes(int64_t R, int64_t C) { return 4 * strips_of(R) * C; }
 
 void launch_finish(const float *P, float *out, int64_t rows, int64_t C, hipStream_t stream) {
   hipLaunchKernelGGL(col_finish, dim3((unsigned)ceil_div(C, kFinCols)), dim3(kFinT), 0, stream, P, out, rows, C);
 }
 
-// NT and V of the register kernels, for rows of U to 16384 elements: a wave a
+// W and V of the register kernels, for rows of U to 16384 elements: a wave a
 // row while its lanes hold the row in four units and there are rows for four
-// waves a CU, else a workgroup of 256 or 1024.  nt 0: the looped kernels.
+// waves a CU; else a workgroup of as many waves as the row fills with the
+// fewest units a thread (3456 bf16: 432 units, 7 waves of one, 4% idle lanes;
+// four waves of two leave 16% idle).  For the backward passes (`sums`), few
+// short rows go to one workgroup, whose column sums need no second launch.
+// v 0: the looped kernels.
 struct RowPlan {
-  int nt, v, bt;
+  int w, v, bt;
   int64_t grid;   // workgroups
 };
-RowPlan row_plan(int64_t R, int64_t C, int U, int64_t waves_per_cu) {
+RowPlan row_plan(int64_t R, int64_t C, int kind, bool sums) {
+  const int U = kind == TGEMM_IN_F32 ? kU<float> : kU<uint16_t>;
   RowPlan p = {0, 0, 0, 0};
   const int64_t nu = ceil_div(C, U);
   if (C < U || C > 16384) return p;
-  p.nt = nu <= 256 && (R >= 1024 || nu <= 64) ? 64 : nu <= 1024 ? 256 : 1024;
-  p.bt = p.nt == 64 ? 256 : p.nt;
-  p.v = (int)ceil_div(nu, p.nt);
-  const int64_t groups = ceil_div(R, p.bt / p.nt);
-  const int64_t cap = kCUs * (64 * waves_per_cu > p.bt ? 64 * waves_per_cu / p.bt : 1);
-  p.grid = groups < cap ? groups : cap;
+  p.w = nu <= 256 && (R >= 1024 || nu <= 64) ? 1 : 0;
+  p.v = (int)ceil_div(nu, p.w ? 64 : 1024);
+  p.bt = p.w ? 256 : 64 * (int)ceil_div(nu, 64 * p.v);
+  if (sums && nu <= 64 && R <= 64) p.bt = 64 * (int)(R < 16 ? R : 16);
+  const int64_t groups = ceil_div(R, p.w ? p.bt / 64 : 1), per_cu = 64 * (sums ? kBwdWaves : kNormWaves) / p.bt;
+  const int64_t cap = kCUs * (per_cu > 1 ? per_cu : 1);
+  p.grid = sums && nu <= 64 && R <= 64 ? 1 : groups < cap ? groups : cap;
   return p;
 }
 
-// the row kernel K<T, NT, V, BT> of a plan
-#define ROW_CASE(NT, V, BT) \
-  case NT * 8 + V: hipLaunchKernelGGL((Kernel::template Of<T, NT, V, BT>::run), g, b, 0, stream, a); break;
+// the row kernel K<T, W, V> of a plan
+#define ROW_CASE(W, V) \
+  case W * 8 + V: hipLaunchKernelGGL((Kernel::template Of<T, W, V>::run), g, b, 0, stream, a); break;
 template <class Kernel, class T>
 void row_launch(const RowPlan &p, const typename Kernel::Args &a, hipStream_t stream) {
   const dim3 g((unsigned)p.grid), b((unsigned)p.bt);
-  switch (p.nt * 8 + p.v) {
-    ROW_CASE(64, 1, 256) ROW_CASE(64, 2, 256) ROW_CASE(64, 3, 256) ROW_CASE(64, 4, 256)
-    ROW_CASE(256, 1, 256) ROW_CASE(256, 2, 256) ROW_CASE(256, 3, 256) ROW_CASE(256, 4, 256)
-    ROW_CASE(1024, 2, 1024)
+  switch (p.w * 8 + p.v) {
+    ROW_CASE(1, 1) ROW_CASE(1, 2) ROW_CASE(1, 3) ROW_CASE(1, 4)
+    ROW_CASE(0, 1) ROW_CASE(0, 2)
     default: break;
   }
   if constexpr (kU<T> == 4) {   // float32 rows past 8192
-    switch (p.nt * 8 + p.v) {
-      ROW_CASE(1024, 3, 1024) ROW_CASE(1024, 4, 1024)
+    switch (p.w * 8 + p.v) {
+      ROW_CASE(0, 3) ROW_CASE(0, 4)
       default: break;
     }
   }
 }
 #undef ROW_CASE
-#define ROW_KERNEL(NAME, KERNEL, ARGS)                                      \
-  struct NAME {                                                             \
-    typedef ARGS Args;                                                      \
-    template <class T, int NT, int V, int BT>                               \
-    struct Of {                                                             \
-      static constexpr auto run = KERNEL<T, NT, V, BT>;                     \
-    };                                                                      \
+#define ROW_KERNEL(NAME, ARGS, ...)                \
+  struct NAME {                                    \
+    typedef ARGS Args;                             \
+    template <class T, int W, int V>               \
+    struct Of {                                    \
+      static constexpr auto run = __VA_ARGS__;     \
+    };                                             \
   };
-ROW_KERNEL(NormReg, norm_reg, NormArgs)
-ROW_KERNEL(NormBwdReg, norm_bwd_reg, NormBwdArgs)
-ROW_KERNEL(EpiBwdReg, epi_bwd_reg, EpiBwdArgs)
+ROW_KERNEL(NormReg, NormArgs, norm_reg<T, W, V>)
+ROW_KERNEL(NormBwdReg, NormBwdArgs, norm_bwd_reg<T, W, V>)
+ROW_KERNEL(EpiBwdPoly, EpiBwdArgs, epi_bwd_reg<T, W, V, 0>)
+ROW_KERNEL(EpiBwdSigm, EpiBwdArgs, epi_bwd_reg<T, W, V, 1>)
 #undef ROW_KERNEL
 template <class Kernel>
 void row_launch(int kind, const RowPlan &p, const typename Kernel::Args &a, hipStream_t stream) {
@@ -997,6 +1043,21 @@ void row_launch(int kind, const RowPlan &p, const typename Kernel::Args &a, hipS
     row_launch<Kernel, float>(p, a, stream);
   else
     row_launch<Kernel, uint16_t>(p, a, stream);
+}
+
+// bytes of P for either kind: a row for each workgroup of the row kernel, or
+// each strip of the looped kernels; none where one workgroup takes every row
+int64_t col_ws_bytes(int64_t R, int64_t C) {
+  int64_t rows = 0;
+  for (const int kind : {TGEMM_IN_F32, TGEMM_IN_BF16}) {
+    const RowPlan p = row_plan(R, C, kind, true);
+    const int64_t n = p.v == 0 ? strips_of(R) : p.grid > 1 ? p.grid : 0;
+    rows = n > rows ? n : rows;
+  }
+  return 4 * rows * C;
+}
+bool workspace_ok(const void *ws, int64_t bytes, int64_t need) {
+  return need == 0 || (ws && bytes >= need && aligned(ws, 16));
 }
 
 template <class T, bool NORM>
@@ -1026,8 +1087,8 @@ int ternary_rmsnorm_quantize(const void *X, int in_kind, const void *residual, c
   const void *const same[5][2] = {{X, residual}};
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
   const NormArgs a = {X, residual, gain, H, Y, rstd, scale, Q, eps, R, C};
-  const RowPlan p = row_plan(R, C, in_kind == TGEMM_IN_F32 ? 4 : 8, kNormWaves);
-  if (p.nt) {
+  const RowPlan p = row_plan(R, C, in_kind, false);
+  if (p.v) {
     row_launch<NormReg>(in_kind, p, a, stream);
     return done();
   }
@@ -1054,16 +1115,16 @@ int ternary_rmsnorm_backward(const void *dY, const void *H, int in_kind, const f
   const int st = check_rc(in_kind, R, C);
   if (st != TGEMM_OK) return st;
   const int64_t wb = col_ws_bytes(R, C);
-  if (!workspace || workspace_bytes < wb || !aligned(workspace, 16)) return TGEMM_ERR_WORKSPACE;
+  if (!workspace_ok(workspace, workspace_bytes, wb)) return TGEMM_ERR_WORKSPACE;
   const int64_t xb = R * C * (in_kind == TGEMM_IN_F32 ? 4 : 2);
-  const Buf outs[] = {{dX, xb}, {dgain, 4 * C}, {workspace, wb}};
+  const Buf outs[] = {{dX, xb}, {dgain, 4 * C}, {workspace, workspace_bytes > 0 ? workspace_bytes : 0}};
   const Buf ins[] = {{dY, xb}, {H, xb}, {gain, 4 * C}, {rstd, 4 * R}, {dH, xb}};
   const void *const same[3][2] = {{dH, dH}};
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
   float *P = static_cast<float *>(workspace);
   NormBwdArgs a = {dY, H, gain, rstd, dH, dX, P, R, C};
-  const RowPlan p = row_plan(R, C, in_kind == TGEMM_IN_F32 ? 4 : 8, kBwdWaves);
-  if (p.nt) {
+  const RowPlan p = row_plan(R, C, in_kind, true);
+  if (p.v) {
     if (p.grid == 1) a.P = dgain;
     row_launch<NormBwdReg>(in_kind, p, a, stream);
     if (p.grid > 1) launch_finish(P, dgain, p.grid, C, stream);
@@ -1094,18 +1155,21 @@ int ternary_epilogue_backward(const void *dY, const void *Z, int in_kind, int ac
   if (st != TGEMM_OK) return st;
   if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_VALUE;
   const int64_t wb = dbias ? col_ws_bytes(R, C) : 0;
-  if (dbias && (!workspace || workspace_bytes < wb || !aligned(workspace, 16))) return TGEMM_ERR_WORKSPACE;
+  if (!workspace_ok(workspace, workspace_bytes, wb)) return TGEMM_ERR_WORKSPACE;
   const int64_t n = R * C, xb = n * (in_kind == TGEMM_IN_F32 ? 4 : 2);
-  const Buf outs[] = {{dZ, xb}, {dbias, 4 * C}, {Q, n}, {scale, 4 * R}, {dbias ? workspace : nullptr, wb}};
+  const Buf outs[] = {{dZ, xb}, {dbias, 4 * C}, {Q, n}, {scale, 4 * R}, {workspace, workspace_bytes > 0 ? workspace_bytes : 0}};
   const Buf ins[] = {{dY, xb}, {Z, xb}};
   const void *const same[5][2] = {};
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
   float *P = static_cast<float *>(workspace);
   EpiBwdArgs a = {dY, Z, dZ, Q, scale, dbias ? P : nullptr, R, C, act};
-  const RowPlan p = row_plan(R, C, in_kind == TGEMM_IN_F32 ? 4 : 8, kBwdWaves);
-  if (p.nt) {
+  const RowPlan p = row_plan(R, C, in_kind, true);
+  if (p.v) {
     if (p.grid == 1) a.P = dbias;
-    row_launch<EpiBwdReg>(in_kind, p, a, stream);
+    if (is_sigm(act))
+      row_launch<EpiBwdSigm>(in_kind, p, a, stream);
+    else
+      row_launch<EpiBwdPoly>(in_kind, p, a, stream);
     if (dbias && p.grid > 1) launch_finish(P, dbias, p.grid, C, stream);
     return done();
   }
