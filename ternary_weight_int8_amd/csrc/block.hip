@@ -30,7 +30,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kNT = 256;   // threads per workgroup
 constexpr int64_t kCUs = 256;                        // compute units of an MI355X
-constexpr int64_t kNormWaves = 32, kBwdWaves = 8;    // waves a CU of the row kernels' grids, at most
+constexpr int64_t kNormWaves = 32, kBwdWaves = 16;   // waves a CU of the row kernels' grids, at most
 
 bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
@@ -494,10 +494,21 @@ __global__ __launch_bounds__(max_t(W, V)) void norm_bwd_reg(NormBwdArgs a) {
   const int grp = W ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   Units<T, W, V> un;
   un.init((int32_t)a.C, t);
-  float gain[V][U], acc[V][U];
+  // past one unit a thread, registers are short and every row reads the gain
+  // again (from the caches)
+  constexpr bool kKeep = V == 1;
+  float kept[U], acc[V][U];
+  if (kKeep && un.on(0)) load_f<U>(a.gain + un.off[0], kept);
+  auto gain_of = [&](int j, float (&g)[U]) {
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) g[i] = kept[i];
+    } else {
+      load_f<U>(a.gain + un.off[j], g);
+    }
+  };
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    if (un.on(j)) load_f<U>(a.gain + un.off[j], gain[j]);
 #pragma unroll
     for (int i = 0; i < U; ++i) acc[j][i] = 0.f;
   }
@@ -523,14 +534,15 @@ __global__ __launch_bounds__(max_t(W, V)) void norm_bwd_reg(NormBwdArgs a) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (un.on(j)) {
-        float d[U], f[U], part_sum = 0.f;
+        float d[U], f[U], gain[U], part_sum = 0.f;
+        gain_of(j, gain);
         unpack(dy[j], d);
         unpack(h[j], f);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           const float g = d[i] * (f[i] * rstd);
           acc[j][i] += g;
-          part_sum = __builtin_fmaf(g, (j == un.last && i < un.dup) ? 0.f : gain[j][i], part_sum);
+          part_sum = __builtin_fmaf(g, (j == un.last && i < un.dup) ? 0.f : gain[i], part_sum);
         }
         sum += part_sum;
       }
@@ -545,11 +557,12 @@ __global__ __launch_bounds__(max_t(W, V)) void norm_bwd_reg(NormBwdArgs a) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (un.on(j)) {
-        float d[U], f[U];
+        float d[U], f[U], gain[U];
+        gain_of(j, gain);
         unpack(dy[j], d);
         unpack(h[j], f);
 #pragma unroll
-        for (int i = 0; i < U; ++i) d[i] = rstd * __builtin_fmaf(-(f[i] * rstd), mean, d[i] * gain[j][i]);
+        for (int i = 0; i < U; ++i) d[i] = rstd * __builtin_fmaf(-(f[i] * rstd), mean, d[i] * gain[i]);
         if (a.dH) {
           unpack(dh[j], f);
 #pragma unroll
@@ -980,8 +993,10 @@ void launch_finish(const float *P, float *out, int64_t rows, int64_t C, hipStrea
 }
 
 // W and V of the register kernels, for rows of U to 16384 elements: a wave a
-// row while its lanes hold the row in four units and there are rows for four
-// waves a CU; else a workgroup of as many waves as the row fills with the
+// row while its lanes hold the row in one unit, or, where no column sums take
+// registers too, in four and there are rows for four waves a CU (16384x1280
+// bf16: 33.6 us, 37.6 with a workgroup a row; its backward pass 46.9 us against
+// 38.1); else a workgroup of as many waves as the row fills with the
 // fewest units a thread (3456 bf16: 432 units, 7 waves of one, 4% idle lanes;
 // four waves of two leave 16% idle).  For the backward passes (`sums`), few
 // short rows go to one workgroup, whose column sums need no second launch.
@@ -995,7 +1010,7 @@ RowPlan row_plan(int64_t R, int64_t C, int kind, bool sums) {
   RowPlan p = {0, 0, 0, 0};
   const int64_t nu = ceil_div(C, U);
   if (C < U || C > 16384) return p;
-  p.w = nu <= 256 && (R >= 1024 || nu <= 64) ? 1 : 0;
+  p.w = nu <= 64 || (nu <= 256 && R >= 1024 && !sums) ? 1 : 0;
   p.v = (int)ceil_div(nu, p.w ? 64 : 1024);
   p.bt = p.w ? 256 : 64 * (int)ceil_div(nu, 64 * p.v);
   if (sums && nu <= 64 && R <= 64) p.bt = 64 * (int)(R < 16 ? R : 16);
@@ -1012,9 +1027,14 @@ template <class Kernel, class T>
 void row_launch(const RowPlan &p, const typename Kernel::Args &a, hipStream_t stream) {
   const dim3 g((unsigned)p.grid), b((unsigned)p.bt);
   switch (p.w * 8 + p.v) {
-    ROW_CASE(1, 1) ROW_CASE(1, 2) ROW_CASE(1, 3) ROW_CASE(1, 4)
-    ROW_CASE(0, 1) ROW_CASE(0, 2)
+    ROW_CASE(1, 1) ROW_CASE(0, 1) ROW_CASE(0, 2)
     default: break;
+  }
+  if constexpr (!Kernel::kSums) {
+    switch (p.w * 8 + p.v) {
+      ROW_CASE(1, 2) ROW_CASE(1, 3) ROW_CASE(1, 4)
+      default: break;
+    }
   }
   if constexpr (kU<T> == 4) {   // float32 rows past 8192
     switch (p.w * 8 + p.v) {
@@ -1024,18 +1044,19 @@ void row_launch(const RowPlan &p, const typename Kernel::Args &a, hipStream_t st
   }
 }
 #undef ROW_CASE
-#define ROW_KERNEL(NAME, ARGS, ...)                \
+#define ROW_KERNEL(NAME, SUMS, ARGS, ...)          \
   struct NAME {                                    \
     typedef ARGS Args;                             \
+    static constexpr bool kSums = SUMS;            \
     template <class T, int W, int V>               \
     struct Of {                                    \
       static constexpr auto run = __VA_ARGS__;     \
     };                                             \
   };
-ROW_KERNEL(NormReg, NormArgs, norm_reg<T, W, V>)
-ROW_KERNEL(NormBwdReg, NormBwdArgs, norm_bwd_reg<T, W, V>)
-ROW_KERNEL(EpiBwdPoly, EpiBwdArgs, epi_bwd_reg<T, W, V, 0>)
-ROW_KERNEL(EpiBwdSigm, EpiBwdArgs, epi_bwd_reg<T, W, V, 1>)
+ROW_KERNEL(NormReg, false, NormArgs, norm_reg<T, W, V>)
+ROW_KERNEL(NormBwdReg, true, NormBwdArgs, norm_bwd_reg<T, W, V>)
+ROW_KERNEL(EpiBwdPoly, true, EpiBwdArgs, epi_bwd_reg<T, W, V, 0>)
+ROW_KERNEL(EpiBwdSigm, true, EpiBwdArgs, epi_bwd_reg<T, W, V, 1>)
 #undef ROW_KERNEL
 template <class Kernel>
 void row_launch(int kind, const RowPlan &p, const typename Kernel::Args &a, hipStream_t stream) {
