@@ -237,6 +237,142 @@ __device__ __forceinline__ void epi_put4(const Out &o, int64_t Cc, int64_t row, 
   store4(o.ptr, o.kind, e, y);
 }
 
+// The epilogue of a wave's FM x FN fragments, four fragments of a row at a
+// time (more than the accumulators' own registers spilled).  Each pass is straight-line code; what depends on the
+// arguments (bias, Z, residual) is decided once a pass, not once an element:
+// with the decisions inside the unrolled elements, the code was over 100 KB
+// and ran 16384x3456x1280 with gelu in 120 us.
+//   0  lanes: from the MFMA layout (lane l: row l % 16, columns 4 (l / 16) ..
+//      + 3) to four neighbouring lanes a row, by ds_bpermute.  float32: 16
+//      bytes a lane, 64 a row.  bfloat16: fragments in pairs, first exchanged
+//      between lane groups (permlane32_swap, permlane16_swap: group g then
+//      holds columns 8 g .. + 3 of the pair's 32 in the first register set, 8 g
+//      + 4 .. + 7 in the second), so that a lane has 8 columns, 16 bytes, and
+//      a row 64; an odd last fragment has 8 bytes a lane
+//   1  z = scaled sum + bias;  2  Z;  3  the activation;  4  + residual;  5  Y
+// GUARD: the tile reaches past the output's last row or column.
+typedef uint32_t v4u_u __attribute__((ext_vector_type(4), aligned(2)));
+
+// fragments F0 .. F0 + N - 1 of fragment row i; `row` is the lane's output row
+template <int E, bool BF, bool GUARD, int F0, int N, int FN>
+__device__ __forceinline__ void epi_run(const Out &o, int64_t Cc, const v4i (&acc)[FN], int64_t row, bool in,
+                                        int64_t c0, int lane, float rs) {
+#pragma clang fp contract(off)   // every kernel rounds alike
+  constexpr int kKind = BF ? OUT_BF16 : OUT_F32;
+  constexpr int kPairs = BF ? N / 2 : 0;           // fragments 2 k, 2 k + 1 for k < kPairs
+  asm volatile("" : "+v"(lane));   // columns and masks anew in each run: kept over all of them they spilled
+  const int p = lane & 3, src = 4 * ((lane >> 2) + 16 * p);
+  auto col_of = [&](int jj) -> int64_t {           // first of the four columns in register set jj
+    return c0 + 16 * F0 + (jj < 2 * kPairs ? 32 * (jj / 2) + 8 * p + 4 * (jj & 1) : 16 * jj + 4 * p);
+  };
+  float y[N][4];
+  auto store = [&](void *base) {
+    if (!in) return;
+#pragma unroll
+    for (int jj = 0; jj < N; ++jj) {
+      const int64_t col = col_of(jj), at = row * Cc + col;
+      const bool pair = BF && jj < 2 * kPairs;
+      if (pair && !(jj & 1) && (!GUARD || col + 7 < Cc)) {
+        const float(&w)[4] = y[jj + 1 < N ? jj + 1 : jj];
+        *reinterpret_cast<v4u_u *>(static_cast<uint16_t *>(base) + at) =
+            v4u_u{bf16_pack(y[jj][0], y[jj][1]), bf16_pack(y[jj][2], y[jj][3]), bf16_pack(w[0], w[1]),
+                  bf16_pack(w[2], w[3])};
+      } else if (pair && (jj & 1) && (!GUARD || col + 3 < Cc)) {
+        // went with the set before it
+      } else if (!GUARD || col + 3 < Cc) {
+        store4(base, kKind, at, y[jj]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < Cc) store1(base, kKind, at + e, y[jj][e]);
+      }
+    }
+  };
+  {
+    v4i v[N];
+#pragma unroll
+    for (int jj = 0; jj < N; ++jj) v[jj] = acc[F0 + jj];
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const auto h = __builtin_amdgcn_permlane32_swap(v[2 * k][e], v[2 * k + 1][e], false, false);
+        const auto q = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+        v[2 * k][e] = q[0];
+        v[2 * k + 1][e] = q[1];
+      }
+#pragma unroll
+    for (int jj = 0; jj < N; ++jj)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[jj][e] = scaled(__builtin_amdgcn_ds_bpermute(src, v[jj][e]), rs, o.cscal);
+  }
+  if (o.bias) {
+#pragma unroll
+    for (int jj = 0; jj < N; ++jj) {
+      const int64_t col = col_of(jj);
+      if (!GUARD || col + 3 < Cc) {
+        const v4f_u b = *reinterpret_cast<const v4f_u *>(o.bias + col);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[jj][e] += b[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < Cc) y[jj][e] += o.bias[col + e];
+      }
+    }
+  }
+  if (o.z) store(o.z);
+  if (E != EPI_POLY || o.act != TGEMM_ACT_NONE) {
+#pragma unroll
+    for (int jj = 0; jj < N; ++jj)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[jj][e] = epi_act<E>(y[jj][e], o.act);
+  }
+  if (o.res && in) {
+#pragma unroll
+    for (int jj = 0; jj < N; ++jj) {
+      const int64_t col = col_of(jj), at = row * Cc + col;
+      if (!GUARD || col + 3 < Cc) {
+        if constexpr (BF) {
+          const v2u_u v = *reinterpret_cast<const v2u_u *>(static_cast<const uint16_t *>(o.res) + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[jj][e] += __uint_as_float(e & 1 ? v[e / 2] & 0xFFFF0000u : v[e / 2] << 16);
+        } else {
+          const v4f_u v = *reinterpret_cast<const v4f_u *>(static_cast<const float *>(o.res) + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[jj][e] += v[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < Cc)
+            y[jj][e] += BF ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(o.res)[at + e] << 16)
+                           : static_cast<const float *>(o.res)[at + e];
+      }
+    }
+  }
+  store(o.ptr);
+  __builtin_amdgcn_sched_barrier(0);   // the next run's registers do not mix with this one's
+}
+
+template <int E, bool BF, bool GUARD, int F0, int FN>
+__device__ __forceinline__ void epi_row(const Out &o, int64_t Cc, const v4i (&acc)[FN], int64_t row, bool in,
+                                        int64_t c0, int lane, float rs) {
+  constexpr int N = FN - F0 < 4 ? FN - F0 : 4;
+  epi_run<E, BF, GUARD, F0, N, FN>(o, Cc, acc, row, in, c0, lane, rs);
+  if constexpr (F0 + N < FN) epi_row<E, BF, GUARD, F0 + N, FN>(o, Cc, acc, row, in, c0, lane, rs);
+}
+
+template <int E, bool BF, bool GUARD, int FM, int FN>
+__device__ __forceinline__ void epi_tile(const Out &o, int64_t R, int64_t Cc, const v4i (&acc)[FM][FN], int64_t r0,
+                                         int64_t c0, int lane, const float (&rs)[FM]) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t row = r0 + (lane >> 2) + 16 * i;
+    epi_row<E, BF, GUARD, 0, FN>(o, Cc, acc[i], row, !GUARD || row < R, c0, lane, rs[i]);
+  }
+}
+
 // columns col .. col + 3 of row `row`, all inside the output (o.vec); r is
 // the row's scale (read by the caller; unused for int32)
 template <int E>
@@ -861,7 +997,7 @@ struct StageBytes {
 // Epilogue: lane holds O[row][col .. col+3] of each 16x16 block of a wave's
 // sub-tile starting at (r0, c0); `inside` says the workgroup's whole tile is
 // inside the output.
-template <class T, int E = EPI_NONE>
+template <class T>
 __device__ __forceinline__ void store_tile(const Args &a, const v4i (&acc)[T::FM][T::FN], int64_t r0,
                                            int64_t c0, bool inside, int lane) {
   const int64_t rbase = r0 + (lane & 15);
@@ -883,7 +1019,7 @@ __device__ __forceinline__ void store_tile(const Args &a, const v4i (&acc)[T::FM
         v4i v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_ds_bpermute(src, acc[i][j][e]);
-        put4<E>(a.o, a.Cc, row, cp + j * 16, v, r);
+        put4<EPI_NONE>(a.o, a.Cc, row, cp + j * 16, v, r);
       }
     }
     return;
@@ -897,17 +1033,33 @@ __device__ __forceinline__ void store_tile(const Args &a, const v4i (&acc)[T::FM
     for (int j = 0; j < T::FN; ++j) {
       const int64_t col = cbase + j * 16;
       if (a.o.vec && col + 3 < a.Cc) {
-        put4<E>(a.o, a.Cc, row, col, acc[i][j], r);
+        put4<EPI_NONE>(a.o, a.Cc, row, col, acc[i][j], r);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (col + e < a.Cc) put1<E>(a.o, a.Cc, row, col + e, acc[i][j][e], r);
+          if (col + e < a.Cc) put1<EPI_NONE>(a.o, a.Cc, row, col + e, acc[i][j][e], r);
       }
     }
   }
 }
 
-template <int OP, class T, bool FAST, int E = EPI_NONE>
+// the same with the epilogue
+template <class T, int E, bool BF>
+__device__ __forceinline__ void store_tile_epi(const Args &a, const v4i (&acc)[T::FM][T::FN], int64_t r0, int64_t c0,
+                                               bool inside, int lane) {
+  float rs[T::FM];
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i) {
+    const int64_t row = r0 + (lane >> 2) + 16 * i;
+    rs[i] = a.o.rs[row < a.R ? row : a.R - 1];
+  }
+  if (inside)
+    epi_tile<E, BF, false>(a.o, a.R, a.Cc, acc, r0, c0, lane, rs);
+  else
+    epi_tile<E, BF, true>(a.o, a.R, a.Cc, acc, r0, c0, lane, rs);
+}
+
+template <int OP, class T, bool FAST, int E = EPI_NONE, bool BF = false>
 __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads), amdgpu_waves_per_eu(T::OCC)))
 void tgemm_kernel(Args a) {
   typedef StageBytes<OP, T> SB;
@@ -972,8 +1124,11 @@ void tgemm_kernel(Args a) {
   for (; g < gfull; ++g) group(g, Flag<true>());
   for (; g < ngroups; ++g) group(g, Flag<false>());
 
-  store_tile<T, E>(a, acc, q0 + wm * T::TM, p0 + wn * T::TN, q0 + T::BM <= a.R && p0 + T::BN <= a.Cc,
-                lane);
+  const bool inside = q0 + T::BM <= a.R && p0 + T::BN <= a.Cc;
+  if constexpr (E == EPI_NONE)
+    store_tile<T>(a, acc, q0 + wm * T::TM, p0 + wn * T::TN, inside, lane);
+  else
+    store_tile_epi<T, E, BF>(a, acc, q0 + wm * T::TM, p0 + wn * T::TN, inside, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -1405,7 +1560,7 @@ __device__ __forceinline__ void fs_decode_write(const uint32_t (&x)[fs::Geo<OP>:
     }
 }
 
-template <int OP, int E = EPI_NONE>
+template <int OP, int E = EPI_NONE, bool BF = false>
 __global__ __attribute__((amdgpu_flat_work_group_size(fs::kNT, fs::kNT), amdgpu_waves_per_eu(2)))
 void tgemm_stream(SArgs a) {
   using namespace fs;
@@ -1626,7 +1781,18 @@ void tgemm_stream(SArgs a) {
     // a one-step tile has not waited for anything issued after its row scales
     if (scaled_out && a.nk < 2) wait_vm<0>();
     const float *rsw = rs_s + TM * wave;
-    if (E == EPI_NONE && a.o.vec8 && m0 + BM <= a.R && n0 + BN <= a.Cc) {
+    if constexpr (E != EPI_NONE) {
+      const int32_t w0 = m0 + wave * TM;
+      float rs[FM];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) rs[i] = rsw[(lane >> 2) + 16 * i];
+      if (m0 + BM <= a.R && n0 + BN <= a.Cc) {
+        epi_tile<E, BF, false>(a.o, a.R, a.Cc, acc, w0, n0, lane, rs);
+        after = BF ? G::kStoresPair : G::kStores;
+      } else {
+        epi_tile<E, BF, true>(a.o, a.R, a.Cc, acc, w0, n0, lane, rs);
+      }
+    } else if (a.o.vec8 && m0 + BM <= a.R && n0 + BN <= a.Cc) {
       // bf16: scale and convert in the MFMA layout (lane l: row l % 16, four
       // columns -> two dwords), then give each lane 8 columns of a fragment
       // pair's 32: lane L takes row L / 4, columns 8 (L % 4) .. + 7 (fragment
@@ -1685,7 +1851,7 @@ void tgemm_stream(SArgs a) {
           v4i v;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_ds_bpermute(src, acc[i][jj][e]);
-          put4<E>(a.o, a.Cc, rp + 16 * i, cp + 16 * jj, v, r);
+          put4<EPI_NONE>(a.o, a.Cc, rp + 16 * i, cp + 16 * jj, v, r);
         }
       }
       after = G::kStores;
@@ -1699,11 +1865,11 @@ void tgemm_stream(SArgs a) {
         for (int jj = 0; jj < FN; ++jj) {
           const int32_t col = cb + 16 * jj;
           if (a.o.vec && col + 3 < a.Cc) {
-            put4<E>(a.o, a.Cc, row, col, acc[i][jj], r);
+            put4<EPI_NONE>(a.o, a.Cc, row, col, acc[i][jj], r);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (col + e < a.Cc) put1<E>(a.o, a.Cc, row, col + e, acc[i][jj][e], r);
+              if (col + e < a.Cc) put1<EPI_NONE>(a.o, a.Cc, row, col + e, acc[i][jj][e], r);
           }
         }
       }
@@ -2234,7 +2400,10 @@ __global__ __launch_bounds__(256) void skinny_dx_sum(const v4i *__restrict__ par
 
 template <int OP, class T, bool FAST, int E>
 hipError_t launch_t(const Args &a, hipStream_t stream) {
-  hipLaunchKernelGGL((tgemm_kernel<OP, T, FAST, E>), dim3(a.tiles), dim3(kThreads), 0, stream, a);
+  if (E != EPI_NONE && a.o.kind == OUT_BF16)
+    hipLaunchKernelGGL((tgemm_kernel<OP, T, FAST, E, E != EPI_NONE>), dim3(a.tiles), dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((tgemm_kernel<OP, T, FAST, E>), dim3(a.tiles), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -2454,6 +2623,14 @@ hipError_t launch_op(const Args &a, int kernel, int tile, bool fast, hipStream_t
   }
 }
 
+template <int E>
+void launch_stream_epi(const SArgs &sa, int grid, hipStream_t stream) {
+  if (sa.o.kind == OUT_BF16)
+    hipLaunchKernelGGL((tgemm_stream<FWD, E, true>), dim3(grid), dim3(fs::kNT), 0, stream, sa);
+  else
+    hipLaunchKernelGGL((tgemm_stream<FWD, E, false>), dim3(grid), dim3(fs::kNT), 0, stream, sa);
+}
+
 // what ternary_gemm_s8_epilogue adds to the scaled forward
 struct EpiArgs {
   const float *bias;
@@ -2627,9 +2804,9 @@ int run(int op, const int8_t *q, const void *p, void *out, int kind, const float
       sa.tiles = sp.tiles;
       sa.nk = (int32_t)(s.L / BK);
       if (epi == EPI_POLY)
-        hipLaunchKernelGGL((tgemm_stream<FWD, EPI_POLY>), dim3(sp.grid), dim3(fs::kNT), 0, stream, sa);
+        launch_stream_epi<EPI_POLY>(sa, sp.grid, stream);
       else if (epi == EPI_SIGM)
-        hipLaunchKernelGGL((tgemm_stream<FWD, EPI_SIGM>), dim3(sp.grid), dim3(fs::kNT), 0, stream, sa);
+        launch_stream_epi<EPI_SIGM>(sa, sp.grid, stream);
       else if (op == FWD)
         hipLaunchKernelGGL(tgemm_stream<FWD>, dim3(sp.grid), dim3(fs::kNT), 0, stream, sa);
       else
