@@ -69,6 +69,10 @@
 namespace {
 
 typedef int32_t v4i __attribute__((ext_vector_type(4)));
+// byte-aligned loads for rows of any length (gfx950 serves unaligned global
+// accesses): 16384x1280x1284 loaded byte by byte took 115 us
+typedef int32_t v4i_u __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32_u __attribute__((aligned(1)));
 
 constexpr int kThreads = 256;  // 4 waves of 64
 constexpr int BK = 64;         // contraction per step (one 16x16x64 MFMA)
@@ -536,11 +540,13 @@ struct CopyOp {
         // branch-free: read an in-bounds chunk (the row start), keep it only if in
         const v4i v = *reinterpret_cast<const v4i *>(gc < L ? p : ptr[i]);
         s.r[i] = gc < L ? v : v4i{0, 0, 0, 0};
-      } else {
+      } else if (full || gc + 16 <= L) {
+        s.r[i] = *reinterpret_cast<const v4i_u *>(p);
+      } else {   // the row's last chunk, partly inside
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int b = 0; b < 16; ++b)
-          if (full || gc + b < L) w[b >> 2] |= (uint32_t)(uint8_t)p[b] << (8 * (b & 3));
+        for (int b = 0; b < 15; ++b)
+          if (gc + b < L) w[b >> 2] |= (uint32_t)(uint8_t)p[b] << (8 * (b & 3));
         s.r[i] = v4i{(int32_t)w[0], (int32_t)w[1], (int32_t)w[2], (int32_t)w[3]};
       }
     }
@@ -595,11 +601,13 @@ struct DecodeOp {
       } else if (FAST) {  // L % 16 == 0, 4-B aligned rows; branch-free as above
         const uint32_t v = *reinterpret_cast<const uint32_t *>(gk < L ? p : ptr[i]);
         s.r[i] = gk < L ? v : 0u;
+      } else if (full || gk + 16 <= L) {
+        s.r[i] = *reinterpret_cast<const u32_u *>(p);
       } else {
         uint32_t w = 0;
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (full || gk + 4 * b < L) w |= (uint32_t)p[b] << (8 * b);
+        for (int b = 0; b < 3; ++b)
+          if (gk + 4 * b < L) w |= (uint32_t)p[b] << (8 * b);
         s.r[i] = w;
       }
     }
@@ -1884,6 +1892,200 @@ void tgemm_stream(SArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// Ring kernel: the forward with its epilogue, one output tile a workgroup, two
+// workgroups a CU.
+//
+// For outputs of too few, or too unevenly many, of the stream kernel's tiles.
+// A CU's two workgroups share nothing and drift apart, so one stores its tile
+// while the other multiplies.  Staging as in the stream kernel (loads straight
+// into LDS, each wave decoding the packed dwords that it loaded, fragments
+// read a step ahead), with rings of D stages for A and D - 1 for the packed
+// codes: step g issues the loads of step g + D, decodes step g + 2 and
+// multiplies step g.  Waits by count (operations of a wave complete in issue
+// order): after the awaited packed codes of step g + 2 come that batch's A loads
+// and D - 2 whole batches, after A(g + 2) the D - 2 batches.  Waves are WM x WN,
+// each TM x TN of the tile.
+// Bound by each step's chain (barrier, fragment reads, decode, barrier; about
+// 1000 cycles for 8 waves on 128 x 128, whose products take 256): without loads
+// and decode 16384x1280x3456 still takes 68 of 107 us, and neither whole-line A
+// loads nor A from the caches alone change it.  Measured beside it (4096x1280x3456
+// f32, 16384x1280x3456 bf16): 4 waves on 128 x 160 42 and 108 us, 8 on 128 x 160
+// 39 and 107, 4 on 64 x 160 42 and 148, 8 on 256 x 128 45 and 108, this 43 and
+// 107; at 2000x2048x2048, where tiles are few, 32, 27, 29, 29 and 20.
+// ---------------------------------------------------------------------------
+namespace rg {
+template <int BM_, int BN_, int WM_, int WN_, int D_>
+struct Cfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, D = D_;
+  static constexpr int NW = WM * WN, NT = 64 * NW, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  static constexpr int kAStage = BM * LP, kALoads = kAStage / 1024 / NW;
+  static constexpr int kWdStage = BN * LP;
+  static constexpr int kUnits = BN / 16, kUnitQ = kUnits / NW, kUnitR = kUnits % NW;   // 64 packed dwords each
+  static constexpr int kWpLoads = kUnitQ + (kUnitR ? 1 : 0), kWpStage = kUnits * 256, PS = D - 1;
+  __host__ __device__ static constexpr int units_of(int w) { return kUnitQ + (w >= NW - kUnitR ? 1 : 0); }
+  __host__ __device__ static constexpr int first_unit(int w) {
+    return kUnitQ * w + (w > NW - kUnitR ? w - (NW - kUnitR) : 0);
+  }
+  static constexpr int kOffWd = D * kAStage, kOffWp = kOffWd + 3 * kWdStage, kLds = kOffWp + PS * kWpStage;
+  static constexpr int kBatch = kALoads + kUnitQ;   // a wave with an extra unit has one more: waiting for fewer is safe
+  static constexpr int kWaitMid = kALoads + (D - 2) * kBatch, kWaitEnd = (D - 2) * kBatch;
+  static constexpr int kPD = 2;                     // weight fragments read ahead
+  static_assert(FM * 16 * WM == BM && FN * 16 * WN == BN && kALoads * 1024 * NW == kAStage, "tile");
+  static_assert(D >= 3 && kUnitQ >= 1 && kWaitMid <= 63 && kPD < FN && kALoads + 1 < FN, "steps");
+  static_assert(first_unit(NW - 1) + units_of(NW - 1) == kUnits && kLds <= 80 * 1024, "units, LDS");
+};
+}  // namespace rg
+
+template <class C, int E, bool BF>
+__global__ __attribute__((amdgpu_flat_work_group_size(C::NT, C::NT), amdgpu_waves_per_eu(2)))
+void tgemm_ring(SArgs a) {
+  using fs::dma4;
+  using fs::dma16;
+  using fs::wait_barrier;
+  using fs::wait_vm;
+  constexpr int FM = C::FM, FN = C::FN, D = C::D, kPD = C::kPD;
+  __shared__ __attribute__((aligned(1024))) int8_t smem[C::kLds];
+  const uint32_t lbase = (uint32_t)(uintptr_t)smem;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int32_t pos = xcd_tile((int32_t)blockIdx.x, a.tiles, a.xcds);
+  const int32_t m0 = pos / a.tiles_c * C::BM, n0 = pos % a.tiles_c * C::BN;
+
+  // load offsets: A load i fills tile rows 16 (kALoads wave + i) + lane / 4, lane
+  // l its slot l % 4; packed load i the dwords 64 u + lane, row d / 4.  Rows and
+  // columns past the output load the last valid one (computed, never stored).
+  uint32_t offA[C::kALoads], offW[C::kWpLoads];
+#pragma unroll
+  for (int i = 0; i < C::kALoads; ++i) {
+    const int r = 16 * (C::kALoads * wave + i) + (lane >> 2);
+    const int32_t m = m0 + r < a.R ? m0 + r : a.R - 1;
+    offA[i] = (uint32_t)(m * a.ldq + 16 * ((lane & 3) ^ ((r >> 1) & 3)));
+  }
+#pragma unroll
+  for (int i = 0; i < C::kWpLoads; ++i) {
+    const int d = 64 * (C::first_unit(wave) + (i < C::units_of(wave) ? i : 0)) + lane;
+    const int32_t n = n0 + (d >> 2) < a.Cc ? n0 + (d >> 2) : a.Cc - 1;
+    offW[i] = (uint32_t)(n * a.kb + 4 * (d & 3));
+  }
+  auto load_w = [&](int ps, int32_t s) {
+    const uint32_t lw = lbase + C::kOffWp + ps * C::kWpStage + 256 * C::first_unit(wave);
+#pragma unroll
+    for (int i = 0; i < C::kWpLoads; ++i)
+      if (i < C::units_of(wave)) dma4(lw + 256 * i, offW[i], a.Wp + 16 * s);
+  };
+  auto load_a = [&](int st, int i, int32_t s) {
+    dma16(lbase + st * C::kAStage + wave * (C::kALoads * 1024) + 1024 * i, offA[i], a.Q + 64 * s);
+  };
+  auto last = [&](int32_t s) { return s < a.nk ? s : a.nk - 1; };   // past the end the last step again, never used
+  auto decode_read = [&](uint32_t (&x)[C::kWpLoads], int ps) {
+    const int8_t *src = smem + C::kOffWp + ps * C::kWpStage;
+#pragma unroll
+    for (int i = 0; i < C::kWpLoads; ++i)
+      if (i < C::units_of(wave))
+        x[i] = *reinterpret_cast<const uint32_t *>(src + 256 * (C::first_unit(wave) + i) + 4 * lane);
+  };
+  auto decode_write = [&](const uint32_t (&x)[C::kWpLoads], int st) {
+    int8_t *dst = smem + C::kOffWd + st * C::kWdStage;
+#pragma unroll
+    for (int i = 0; i < C::kWpLoads; ++i)
+      if (i < C::units_of(wave)) {
+        const int d = 64 * (C::first_unit(wave) + i) + lane;
+        *reinterpret_cast<v4i *>(dst + swz(d >> 2, d & 3)) = decode16(x[i]);
+      }
+  };
+
+  v4i acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int jj = 0; jj < FN; ++jj) acc[i][jj] = v4i{0, 0, 0, 0};
+
+  // steps 0 .. D - 2 go out; 0 and 1 are decoded, which frees packed stage 0 for
+  // step D - 1
+#pragma unroll
+  for (int s = 0; s < D - 1; ++s) {
+    load_w(s, last(s));
+#pragma unroll
+    for (int i = 0; i < C::kALoads; ++i) load_a(s, i, last(s));
+  }
+  wait_vm<C::kALoads + (D - 3) * C::kBatch>();
+  {
+    uint32_t x0[C::kWpLoads], x1[C::kWpLoads];
+    decode_read(x0, 0);
+    decode_read(x1, 1);
+    decode_write(x0, 0);
+    decode_write(x1, 1);
+  }
+  load_w(0, last(D - 1));
+#pragma unroll
+  for (int i = 0; i < C::kALoads; ++i) load_a(D - 1, i, last(D - 1));
+  wait_barrier<C::kWaitEnd>();
+
+  const int qoff = wm * C::TM * LP + swz(lane & 15, lane >> 4);
+  const int poff = C::kOffWd + wn * C::TN * LP + swz(lane & 15, lane >> 4);
+  v4i qc[FM], pf[FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) qc[i] = *reinterpret_cast<const v4i *>(smem + qoff + i * 16 * LP);
+#pragma unroll
+  for (int jj = 0; jj < kPD; ++jj) pf[jj] = *reinterpret_cast<const v4i *>(smem + poff + jj * 16 * LP);
+  // every wave's reads of A stage 0 are done before step 0 loads into it
+  wait_barrier<C::kWaitEnd>();
+
+  int q0 = 0, w0 = 0, pl = 1 % C::PS, pd = 2 % C::PS;   // stages: A and decoded of step g, packed of g + D and g + 2
+  for (int32_t g = 0; g < a.nk; ++g) {
+    const int q1 = q0 + 1 == D ? 0 : q0 + 1, w1 = w0 == 2 ? 0 : w0 + 1, w2 = w1 == 2 ? 0 : w1 + 1;
+    const int32_t sl = last(g + D);
+    const int8_t *pc = smem + poff + w0 * C::kWdStage, *pn_ = smem + poff + w1 * C::kWdStage;
+    const int8_t *qn_ = smem + qoff + q1 * C::kAStage;
+    v4i qn[FM], pn[kPD];
+    uint32_t x[C::kWpLoads];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) qn[i] = *reinterpret_cast<const v4i *>(qn_ + i * 16 * LP);
+#pragma unroll
+    for (int jj = 0; jj < FN; ++jj) {
+      if (jj == 0) load_w(pl, sl);
+      if (jj >= 1 && jj <= C::kALoads) load_a(q0, jj - 1, sl);
+      if (jj + kPD < FN)
+        pf[jj + kPD] = *reinterpret_cast<const v4i *>(pc + (jj + kPD) * 16 * LP);
+      else
+        pn[jj + kPD - FN] = *reinterpret_cast<const v4i *>(pn_ + (jj + kPD - FN) * 16 * LP);
+      if (jj == C::kALoads + 1) {
+        wait_vm<C::kWaitMid>();
+        decode_read(x, pd);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        acc[i][jj] = __builtin_amdgcn_mfma_i32_16x16x64_i8(pf[jj], qc[i], acc[i][jj], 0, 0, 0);
+    }
+    decode_write(x, w2);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) qc[i] = qn[i];
+#pragma unroll
+    for (int jj = 0; jj < kPD; ++jj) pf[jj] = pn[jj];
+    wait_barrier<C::kWaitEnd>();
+    q0 = q1;
+    w0 = w1;
+    pl = pl + 1 == C::PS ? 0 : pl + 1;
+    pd = pd + 1 == C::PS ? 0 : pd + 1;
+  }
+
+  const int32_t r0 = m0 + wm * C::TM, c0 = n0 + wn * C::TN;
+  float rs[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int32_t row = r0 + (lane >> 2) + 16 * i;
+    rs[i] = a.o.rs[row < a.R ? row : a.R - 1];
+  }
+  if (m0 + C::BM <= a.R && n0 + C::BN <= a.Cc)
+    epi_tile<E, BF, false>(a.o, a.R, a.Cc, acc, r0, c0, lane, rs);
+  else
+    epi_tile<E, BF, true>(a.o, a.R, a.Cc, acc, r0, c0, lane, rs);
+  // no transfer into LDS may outlive the workgroup
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // Skinny forward kernel (tgemm_skinny): C[M][N] with at most 32 rows.  Here
 // the packed weights are nearly all of the bytes moved, so the product is
 // bound by reading them from HBM, and keeping W as 2-bit codes reads a
@@ -2623,6 +2825,34 @@ hipError_t launch_op(const Args &a, int kernel, int tile, bool fast, hipStream_t
   }
 }
 
+typedef rg::Cfg<128, 128, 4, 2, 4> Ring;
+
+// Whether the epilogue's forward runs the ring kernel: the stream kernel's
+// alignment and 32-bit offsets, and tiles for three quarters of the CUs at
+// least (fewer 128 x 128 tiles leave more idle than 64 x 64 ones of the tiled
+// kernel: 1000x1000x1024 14 against 12 us, 8000x500x1024 16 against 24 us).
+// The persistent stream kernel stays ahead where its 512 x 144 tiles fill its
+// rounds (16384x3456x1280 with gelu: 113 against 132 us; at 16384x1280x3456, 288
+// tiles for 256 CUs, 146 against 107 us), and so do the tiled kernel's 256 x 128
+// tiles where they fill the chip exactly, two a CU (4096x4096x4096: 80 against
+// 90 us).
+bool filled(int64_t tiles, int64_t slots) { return 4 * tiles >= 3 * ceil_div(tiles, slots) * slots; }
+bool ring_ok(int64_t M, int64_t N, int64_t K, const void *A, const void *W, const StreamPlan &sp, const Machine &mc) {
+  if (K % BK != 0 || !aligned(A, 16) || !aligned(W, 4) || M > INT32_MAX / K || N > INT32_MAX / (K / 4)) return false;
+  const int64_t tiles = ceil_div(M, Ring::BM) * ceil_div(N, Ring::BN);
+  const int64_t large = ceil_div(M, TileShapes::L::BM) * ceil_div(N, TileShapes::L::BN);
+  if (tiles > INT32_MAX || 4 * tiles < 3 * mc.cus) return false;
+  return sp.ok ? !filled(sp.tiles, sp.grid) : large % (2 * mc.cus) != 0;
+}
+
+template <int E>
+void launch_ring(const SArgs &sa, hipStream_t stream) {
+  if (sa.o.kind == OUT_BF16)
+    hipLaunchKernelGGL((tgemm_ring<Ring, E, true>), dim3(sa.tiles), dim3(Ring::NT), 0, stream, sa);
+  else
+    hipLaunchKernelGGL((tgemm_ring<Ring, E, false>), dim3(sa.tiles), dim3(Ring::NT), 0, stream, sa);
+}
+
 template <int E>
 void launch_stream_epi(const SArgs &sa, int grid, hipStream_t stream) {
   if (sa.o.kind == OUT_BF16)
@@ -2789,7 +3019,8 @@ int run(int op, const int8_t *q, const void *p, void *out, int kind, const float
   }
   {
     const StreamPlan sp = stream_plan(op, M, N, K, align_of(q), align_of(p), mc);
-    if (sp.ok) {
+    const bool ring = epi != EPI_NONE && ring_ok(M, N, K, q, p, sp, mc);
+    if (sp.ok || ring) {
       SArgs sa;
       sa.xcds = mc.xcds;
       sa.Q = q;
@@ -2803,7 +3034,14 @@ int run(int op, const int8_t *q, const void *p, void *out, int kind, const float
       sa.tiles_c = sp.tiles_c;
       sa.tiles = sp.tiles;
       sa.nk = (int32_t)(s.L / BK);
-      if (epi == EPI_POLY)
+      if (ring) {
+        sa.tiles_c = (int32_t)ceil_div(N, Ring::BN);
+        sa.tiles = (int32_t)(ceil_div(M, Ring::BM) * sa.tiles_c);
+        if (epi == EPI_POLY)
+          launch_ring<EPI_POLY>(sa, stream);
+        else
+          launch_ring<EPI_SIGM>(sa, stream);
+      } else if (epi == EPI_POLY)
         launch_stream_epi<EPI_POLY>(sa, sp.grid, stream);
       else if (epi == EPI_SIGM)
         launch_stream_epi<EPI_SIGM>(sa, sp.grid, stream);
