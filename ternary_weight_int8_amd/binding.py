@@ -726,28 +726,33 @@ def ternary_clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None, works
     """(out, norm float32 [1]): the gradients scaled by min(1, max_norm / (norm
     + eps)), norm the root of the sum of all their squares.  grads is a list of
     contiguous float32 or bfloat16 device tensors of any shapes, on one device;
-    out a list of such tensors (`grads` itself: in place), new ones if None."""
+    out a list of tensors of the same types and sizes (`grads` itself: in
+    place), new ones if None."""
     torch = _torch()
     grads = list(grads)
     if not grads:
         raise ValueError("grads must hold at least one tensor")
     n = len(grads)
-    kinds = [_kind(g, "every gradient") for g in grads]
-    dev = grads[0].device
-    for i, g in enumerate(grads):
-        if not (g.is_cuda and g.device == dev and g.is_contiguous()):
-            raise ValueError(f"grads[{i}] must be a contiguous tensor on the device of grads[0]")
+    # many tensors, little time: one comprehension a property
+    if not all([isinstance(g, torch.Tensor) for g in grads]):
+        raise TypeError("grads must hold torch.Tensors")
+    types, dev, idx = [g.dtype for g in grads], grads[0].device, grads[0].get_device()
+    kind_of = {torch.float32: IN_F32, torch.bfloat16: IN_BF16}
+    if not kind_of.keys() >= set(types):
+        raise TypeError("grads must be float32 or bfloat16 tensors")
+    if idx < 0 or not all([g.get_device() == idx and g.is_contiguous() for g in grads]):
+        raise ValueError("grads must be contiguous tensors on one GPU device")
+    src, sizes = [g.data_ptr() for g in grads], [g.numel() for g in grads]
     if out is None:
         out = [_like(None, g, stream, "out") for g in grads]
-    else:
-        if len(out) != n:
-            raise ValueError(f"out must hold {n} tensors, got {len(out)}")
-        if out is not grads:
-            for i, g in enumerate(grads):
-                _given(out[i], g.dtype, g.shape, dev, f"out[{i}]")
-    p = ctypes.c_void_p * n
-    src, dst = p(*[g.data_ptr() for g in grads]), p(*[o.data_ptr() for o in out])
-    sizes, kinds = (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int32 * n)(*kinds)
+    elif len(out) != n:
+        raise ValueError(f"out must hold {n} tensors, got {len(out)}")
+    elif not all([isinstance(o, torch.Tensor) and o.dtype == t and o.get_device() == idx and o.is_contiguous()
+                  and o.numel() == s for o, t, s in zip(out, types, sizes)]):
+        raise ValueError("out must hold contiguous tensors of the types and sizes of grads, on their device")
+    dst = [o.data_ptr() for o in out]
+    p, i64 = ctypes.c_void_p * n, ctypes.c_int64 * n
+    src, dst, sizes, kinds = p(*src), p(*dst), i64(*sizes), (ctypes.c_int32 * n)(*[kind_of[t] for t in types])
     norm = _made(norm, torch.float32, (1,), dev, "norm", stream)
     ws = _scratch(workspace, _queried("ternary_clip_grad_norm_workspace", sizes, n), dev, stream)
     _done("ternary_clip_grad_norm",

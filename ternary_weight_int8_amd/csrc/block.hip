@@ -788,6 +788,11 @@ int64_t strips_of(int64_t R) { return R < kMaxStrips ? R : kMaxStrips; }
 // ---------------------------------------------------------------------------
 constexpr int kGroup = 96;                 // tensors per launch
 constexpr int kChunk = 8 * kNT * 4;        // elements per workgroup and step, at most
+// Lists of more bytes than this are written past the caches (a nontemporal
+// store), which leaves the gradients that the second pass reads in them: 80 MB
+// of bf16 29.2 -> 27.8 us, 278 MB 92 -> 78 us, 556 MB of float32 168 -> 140 us.
+// Smaller ones stay cached for whatever reads them next.
+constexpr int64_t kStreamBytes = 32 << 20;
 constexpr int64_t kMaxParts = 1024;        // workgroups of the first pass, over all launches (and one each)
 
 // the tensors of one launch; first[i]: the first chunk of tensor i
@@ -863,7 +868,8 @@ __global__ __launch_bounds__(kNT) void sumsq(Tensors ts, double *__restrict__ pa
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-template <class T>
+// STREAM: the outputs bypass the caches
+template <class T, bool STREAM>
 __device__ __forceinline__ void chunk_scale(const T *p, T *q, int64_t e0, int64_t e1, float f) {
   constexpr int U = kU<T>;
   const int n = (int)(e1 - e0), nu = n / U;
@@ -881,7 +887,11 @@ __device__ __forceinline__ void chunk_scale(const T *p, T *q, int64_t e0, int64_
         unpack(r[k], v);
 #pragma unroll
         for (int i = 0; i < U; ++i) v[i] *= f;
-        store_raw(q + (u0 + k * kNT) * U, pack(v));
+        typename Raw<T>::V *to = reinterpret_cast<typename Raw<T>::V *>(q + (u0 + k * kNT) * U);
+        if constexpr (STREAM)
+          __builtin_nontemporal_store(pack(v), to);
+        else
+          *to = pack(v);
       }
   }
   const int e = nu * U + (int)threadIdx.x;
@@ -889,6 +899,7 @@ __device__ __forceinline__ void chunk_scale(const T *p, T *q, int64_t e0, int64_
 }
 
 // `parts` doubles from the first pass; workgroup 0 of the first launch writes the norm
+template <bool STREAM>
 __global__ __launch_bounds__(kNT) void scale_all(Tensors ts, const double *__restrict__ part, int32_t parts,
                                                  float max_norm, float eps, float *__restrict__ norm) {
   __shared__ double wsum[4];
@@ -905,9 +916,9 @@ __global__ __launch_bounds__(kNT) void scale_all(Tensors ts, const double *__res
     const int64_t e0 = (int64_t)(c - ts.first[i]) * kChunk;
     const int64_t e1 = e0 + kChunk < ts.size[i] ? e0 + kChunk : ts.size[i];
     if (ts.bf16[i])
-      chunk_scale(static_cast<const uint16_t *>(ts.in[i]), static_cast<uint16_t *>(ts.out[i]), e0, e1, f);
+      chunk_scale<uint16_t, STREAM>(static_cast<const uint16_t *>(ts.in[i]), static_cast<uint16_t *>(ts.out[i]), e0, e1, f);
     else
-      chunk_scale(static_cast<const float *>(ts.in[i]), static_cast<float *>(ts.out[i]), e0, e1, f);
+      chunk_scale<float, STREAM>(static_cast<const float *>(ts.in[i]), static_cast<float *>(ts.out[i]), e0, e1, f);
   }
 }
 
@@ -1263,14 +1274,17 @@ int ternary_clip_grad_norm(const void *const *grads, void *const *outs, const in
     hipLaunchKernelGGL(sumsq, dim3((unsigned)grid), dim3(kNT), 0, stream, ts, part + parts);
     parts += grid;
   }
+  int64_t bytes = 0;
+  for (int64_t i = 0; i < count; ++i) bytes += sizes[i] * (kinds[i] == TGEMM_IN_F32 ? 4 : 2);
+  const bool big = bytes > kStreamBytes;
   bool first = true;
   for (int64_t g0 = (count - 1) / kGroup * kGroup; g0 >= 0; g0 -= kGroup) {
     if (count > kGroup || total == 0) fill(ts, grads, outs, sizes, kinds, g0, count);
     const int64_t chunks = ts.first[ts.count];
     if (chunks == 0 && !(first && g0 == 0)) continue;
     const int64_t cap = kCUs * 8, grid = chunks < 1 ? 1 : chunks < cap ? chunks : cap;
-    hipLaunchKernelGGL(scale_all, dim3((unsigned)grid), dim3(kNT), 0, stream, ts, part, (int32_t)parts, max_norm, eps,
-                       first ? norm : nullptr);
+    hipLaunchKernelGGL(big ? scale_all<true> : scale_all<false>, dim3((unsigned)grid), dim3(kNT), 0, stream, ts, part,
+                       (int32_t)parts, max_norm, eps, first ? norm : nullptr);
     first = false;
   }
   return done();
