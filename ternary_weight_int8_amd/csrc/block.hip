@@ -1026,7 +1026,12 @@ RowPlan row_plan(int64_t R, int64_t C, int kind, bool sums) {
   p.bt = p.w ? 256 : 64 * (int)ceil_div(nu, 64 * p.v);
   if (sums && nu <= 64 && R <= 64) p.bt = 64 * (int)(R < 16 ? R : 16);
   const int64_t groups = ceil_div(R, p.w ? p.bt / 64 : 1), per_cu = 64 * (sums ? kBwdWaves : kNormWaves) / p.bt;
-  const int64_t cap = kCUs * (per_cu > 1 ? per_cu : 1);
+  int64_t cap = kCUs * (per_cu > 1 ? per_cu : 1);
+  // column sums: at least four rows a workgroup, down to two workgroups a CU (a
+  // row of P costs as much as half a row: 1782x729 f32, 1280 workgroups 14.3 us,
+  // 512 12.1 us)
+  const int64_t least = R / 4 > 2 * kCUs ? R / 4 : 2 * kCUs;
+  if (sums && cap > least) cap = least;
   p.grid = sums && nu <= 64 && R <= 64 ? 1 : groups < cap ? groups : cap;
   return p;
 }
