@@ -2,6 +2,10 @@
 // GEMM library.  The ABI and the stored-weight format are documented in
 // include/ternary_gemm.h.
 //
+// The forward with its epilogue (ternary_gemm_s8_epilogue: bias, activation,
+// residual) runs the same kernels with another end, EPI_* below, and one
+// kernel of its own for mid-size outputs, tgemm_ring.
+//
 // Sources (cited by page title and section):
 //   [P10425] t27 pull request #10425, "t27c PTX backend: ternary x int8 GEMM
 //            kernel emitted by a .t27 spec (int8 mma.sync), ptx-run glue".
@@ -179,7 +183,7 @@ __device__ __forceinline__ float epi_act(float z, int act) {
     // brings back a NaN that it drops.
     const bool silu = act == TGEMM_ACT_SILU;
     const float k0 = silu ? -kLog2e : -kGeluA * kLog2e, k1 = silu ? 0.f : -kGeluAB * kLog2e;
-    const float c = fminf(fmaxf(z, -200.f), 200.f);
+    const float c = __builtin_amdgcn_fmed3f(z, -200.f, 200.f);
     const float t = c * __builtin_fmaf(k1, c * c, k0);
     return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t));
   }

@@ -292,6 +292,27 @@ def test_product_epilogue_misaligned(M, N, K, kind, offset):
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (act, whole)
 
 
+# the persistent kernel with ragged last tiles, and the one of mid-size outputs
+# over many steps, ragged and not
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,N,K", [(15001, 2301, 128), (14900, 2304, 64), (3001, 1250, 1088), (4096, 1280, 3456), (2048, 2048, 320)])
+def test_product_epilogue_large(M, N, K, kind):
+    say(f"product epilogue {M}x{N}x{K} {kind}")
+    dt = KINDS[kind]
+    A, Wp, rs, ws, bias, res = product_inputs(M, N, K, dt, kind, 7)
+    p = Placed(8)
+    for act, r, save in (("relu2", res, True), ("gelu_tanh", None, True), ("silu", res, False)):
+        z, ez, y, ey = ref.product(A, Wp, rs, float(torch.tensor(ws)), bias, act, r)
+        Y, Z = B.ternary_gemm_s8_epilogue(A, Wp, rs, ws, bias=bias, act=act, residual=r, out_dtype=dt, save=save,
+                                          Y=p((M, N), dt), Z=p((M, N), dt) if save else None)
+        torch.cuda.synchronize()
+        p.check()
+        p.made.clear()
+        ref.check(Y, y, ref.rounded(y, ey, dt), f"{act}: Y")
+        if save:
+            ref.check(Z, z, ref.rounded(z, ez, dt), f"{act}: Z")
+
+
 def test_product_epilogue_not_finite_stays_by_itself():
     say("product epilogue not finite")
     M, N, K = 40, 48, 64
