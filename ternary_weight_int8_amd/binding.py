@@ -556,11 +556,12 @@ def _made(t, dtype, shape, device, what, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _like(t, x, stream, what):
-    """The caller's output of x's type and shape, or a new one."""
+def _like(t, x, stream, what, dtype=None):
+    """The caller's output of x's shape and of dtype (x's), or a new one."""
+    dtype = dtype or x.dtype
     if t is None and stream is None:
-        return _torch().empty_like(x)
-    return _made(t, x.dtype, x.shape, x.device, what, stream)
+        return _torch().empty_like(x, dtype=dtype)
+    return _made(t, dtype, x.shape, x.device, what, stream)
 
 
 def _scratch(workspace, nbytes, device, stream):
@@ -630,7 +631,7 @@ def ternary_rmsnorm_quantize(X, gain, eps=1e-6, residual=None, save=False, H=Non
     if save:
         Y = _like(Y, X, stream, "Y")
         rstd = _made(rstd, torch.float32, (R,), dev, "rstd", stream)
-    Q = _made(Q, torch.int8, (R, C), dev, "Q", stream)
+    Q = _like(Q, X, stream, "Q", torch.int8)
     scale = _made(scale, torch.float32, (R,), dev, "scale", stream)
     _done("ternary_rmsnorm_quantize",
           lib().ternary_rmsnorm_quantize(X.data_ptr(), kind, _ptr(residual), gain.data_ptr(), eps,
@@ -653,7 +654,7 @@ def ternary_rmsnorm_backward(dY, H, gain, rstd, dH=None, dX=None, dgain=None, wo
     if dH is not None:
         _given(dH, dt, (R, C), dev, "dH")
     dX = _like(dX, H, stream, "dX")
-    dgain = _made(dgain, torch.float32, (C,), dev, "dgain", stream)
+    dgain = _like(dgain, gain, stream, "dgain")
     ws = _scratch(workspace, _queried("ternary_rmsnorm_backward_workspace", R, C), dev, stream)
     _done("ternary_rmsnorm_backward",
           lib().ternary_rmsnorm_backward(dY.data_ptr(), H.data_ptr(), kind, gain.data_ptr(), rstd.data_ptr(),
@@ -673,10 +674,10 @@ def ternary_gemm_s8_epilogue(A, Wpacked, a_row_scale, w_scale, bias=None, act="n
     _check(A, torch.int8, 2, "A")
     _check(Wpacked, torch.uint8, 2, "Wpacked")
     (M, K), dev = A.shape, A.device
-    N = Wpacked.shape[0]
-    _given(Wpacked, torch.uint8, (N, K // 4), dev, "Wpacked")
-    if K % 4:
-        raise ValueError(f"Wpacked must be [N][K/4] = [{N}][{K // 4}], got {tuple(Wpacked.shape)}")
+    N, kb = Wpacked.shape
+    if kb * 4 != K or Wpacked.device != dev:
+        raise ValueError(f"Wpacked must be [N][K/4] = [{N}][{K // 4}] on {dev}, got {tuple(Wpacked.shape)} on "
+                         f"{Wpacked.device}")
     _given(a_row_scale, torch.float32, (M,), dev, "a_row_scale")
     if bias is not None:
         _given(bias, torch.float32, (N,), dev, "bias")
@@ -713,7 +714,7 @@ def ternary_epilogue_backward(dY, Z, act="none", bias=True, dZ=None, dbias=None,
         ws = _scratch(workspace, _queried("ternary_epilogue_backward_workspace", R, C), dev, stream)
     elif dbias is not None:
         raise ValueError("dbias is an output of bias=True")
-    Q = _made(Q, torch.int8, (R, C), dev, "Q", stream)
+    Q = _like(Q, Z, stream, "Q", torch.int8)
     scale = _made(scale, torch.float32, (R,), dev, "scale", stream)
     _done("ternary_epilogue_backward",
           lib().ternary_epilogue_backward(dY.data_ptr(), Z.data_ptr(), kind, act, dZ.data_ptr(), _ptr(dbias),
