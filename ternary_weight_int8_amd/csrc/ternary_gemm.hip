@@ -249,7 +249,12 @@ __device__ __forceinline__ void epi_put4(const Out &o, int64_t Cc, int64_t row, 
 // time (more than the accumulators' own registers spilled).  Each pass is straight-line code; what depends on the
 // arguments (bias, Z, residual) is decided once a pass, not once an element:
 // with the decisions inside the unrolled elements, the code was over 100 KB
-// and ran 16384x3456x1280 with gelu in 120 us.
+// and ran 16384x3456x1280 with gelu in 120 us.  It takes 111 us now, 84 us
+// without activation and Z: 21 us a tile for the products as in the plain
+// forward, and per wave and tile 144 elements of some 17 vector instructions,
+// which no MFMA covers, since the CU's waves reach their tiles' ends together.
+// Four fragments' lane moves issued ahead of the run before cost registers (spills, 117
+// us), and two workgroups of 256 x 144 a CU, which drift apart, 123 us.
 //   0  lanes: from the MFMA layout (lane l: row l % 16, columns 4 (l / 16) ..
 //      + 3) to four neighbouring lanes a row, by ds_bpermute.  float32: 16
 //      bytes a lane, 64 a row.  bfloat16: fragments in pairs, first exchanged
@@ -2624,6 +2629,7 @@ hipError_t launch_f(const Args &a, bool fast, hipStream_t stream) {
 //          tile with a contraction of 8 steps or more
 //   stream tgemm_stream: large forward and dX outputs (stream_plan)
 //   skinny tgemm_skinny: forward with at most 32 rows (skinny_plan)
+//   ring   tgemm_ring: the forward with its epilogue on mid-size outputs (ring_ok)
 // (A variant that loads the int8 operand of the forward and dX straight into
 // MFMA registers, without LDS, measured no faster in the three-product step
 // on MI355X and was left out.)
@@ -2836,7 +2842,7 @@ typedef rg::Cfg<128, 128, 4, 2, 4> Ring;
 // least (fewer 128 x 128 tiles leave more idle than 64 x 64 ones of the tiled
 // kernel: 1000x1000x1024 14 against 12 us, 8000x500x1024 16 against 24 us).
 // The persistent stream kernel stays ahead where its 512 x 144 tiles fill its
-// rounds (16384x3456x1280 with gelu: 113 against 132 us; at 16384x1280x3456, 288
+// rounds (16384x3456x1280 with gelu: 111 against 132 us; at 16384x1280x3456, 288
 // tiles for 256 CUs, 146 against 107 us), and so do the tiled kernel's 256 x 128
 // tiles where they fill the chip exactly, two a CU (4096x4096x4096: 80 against
 // 90 us).
