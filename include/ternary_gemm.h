@@ -268,8 +268,8 @@ int ternary_quantize_cols(const void *X, int in_kind, int8_t *Q, float *scale, i
  *     a fixed order without atomics: repeated calls give identical bits;
  *   - int8 rows and their scales are what ternary_quantize_rows would make of
  *     the float32 values before they are rounded to the kind: s = max|y| / 127,
- *     q = clamp(rint(y / s), -127, 127), q = 0 where s is 0 or not finite.  A
- *     row that holds an infinity or a NaN has it as its scale;
+ *     q = clamp(rint(y / s), -127, 127), q = 0 where s is 0 or not finite.  The
+ *     scale of a row that holds an infinity or a NaN is not finite;
  *   - a call that needs a workspace takes caller-owned DEVICE memory, 16-byte
  *     aligned, of at least the bytes that the query beside it gives
  *     (TGEMM_ERR_WORKSPACE otherwise; where that is 0, NULL will do).  Its

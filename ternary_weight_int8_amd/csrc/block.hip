@@ -15,7 +15,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <new>
 #include <vector>
 
 #include "ternary_gemm.h"
@@ -1270,7 +1269,7 @@ int ternary_clip_grad_norm(const void *const *grads, void *const *outs, const in
   }
   try {
     if (lists_overlap(grads, outs, sizes, kinds, count)) return TGEMM_ERR_ALIAS;
-  } catch (const std::bad_alloc &) {
+  } catch (...) {
     return TGEMM_ERR_DIM;   // more gradients than the host can list
   }
   if (overlap(norm, 4, workspace, need)) return TGEMM_ERR_ALIAS;
