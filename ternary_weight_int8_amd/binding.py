@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 from .build import LIB
 
@@ -735,25 +736,33 @@ def ternary_clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None, works
         raise ValueError("grads must hold at least one tensor")
     n = len(grads)
     # many tensors, little time: one comprehension a property
-    if not all([isinstance(g, torch.Tensor) for g in grads]):
-        raise TypeError("grads must hold torch.Tensors")
-    types, dev, idx = [g.dtype for g in grads], grads[0].device, grads[0].get_device()
-    kind_of = {torch.float32: IN_F32, torch.bfloat16: IN_BF16}
-    if not kind_of.keys() >= set(types):
+    try:
+        types, idx, sizes = [g.dtype for g in grads], grads[0].get_device(), [g.numel() for g in grads]
+        kinds = [IN_F32 if t is torch.float32 else IN_BF16 if t is torch.bfloat16 else None for t in types]
+        fits = all([g.get_device() == idx and g.is_contiguous() for g in grads])
+        src = [g.data_ptr() for g in grads]
+    except AttributeError:
+        raise TypeError("grads must hold torch.Tensors") from None
+    if None in kinds:
         raise TypeError("grads must be float32 or bfloat16 tensors")
-    if idx < 0 or not all([g.get_device() == idx and g.is_contiguous() for g in grads]):
+    if idx < 0 or not fits:
         raise ValueError("grads must be contiguous tensors on one GPU device")
-    src, sizes = [g.data_ptr() for g in grads], [g.numel() for g in grads]
+    dev = grads[0].device
     if out is None:
         out = [_like(None, g, stream, "out") for g in grads]
     elif len(out) != n:
         raise ValueError(f"out must hold {n} tensors, got {len(out)}")
-    elif not all([isinstance(o, torch.Tensor) and o.dtype == t and o.get_device() == idx and o.is_contiguous()
-                  and o.numel() == s for o, t, s in zip(out, types, sizes)]):
-        raise ValueError("out must hold contiguous tensors of the types and sizes of grads, on their device")
-    dst = [o.data_ptr() for o in out]
-    p, i64 = ctypes.c_void_p * n, ctypes.c_int64 * n
-    src, dst, sizes, kinds = p(*src), p(*dst), i64(*sizes), (ctypes.c_int32 * n)(*[kind_of[t] for t in types])
+    else:
+        try:
+            fits = ([o.dtype for o in out] == types and [o.numel() for o in out] == sizes
+                    and all([o.get_device() == idx and o.is_contiguous() for o in out]))
+        except AttributeError:
+            raise TypeError("out must hold torch.Tensors") from None
+        if not fits:
+            raise ValueError("out must hold contiguous tensors of the types and sizes of grads, on their device")
+    # the C call's four host arrays, alive until it returns
+    arrays = (array("q", src), array("q", [o.data_ptr() for o in out]), array("q", sizes), array("i", kinds))
+    src, dst, sizes, kinds = [a.buffer_info()[0] for a in arrays]
     norm = _made(norm, torch.float32, (1,), dev, "norm", stream)
     ws = _scratch(workspace, _queried("ternary_clip_grad_norm_workspace", sizes, n), dev, stream)
     _done("ternary_clip_grad_norm",
