@@ -391,7 +391,7 @@ const char *ternary_gemm_status_str(int status);
  * which kernel runs (TGEMM_KERNEL_*), and that kernel's threads and LDS bytes
  * per workgroup.  The plan is that of the calls without a workspace and
  * without an epilogue (ternary_gemm_s8_epilogue follows the forward's plan but
- * for mid-size outputs, which have a kernel of their own).
+ * for mid-size outputs, which have a kernel of their own or smaller tiles).
  * Returns TGEMM_OK, or the status the real call would return for these
  * dimensions (pointer checks excepted).
  */

@@ -2871,6 +2871,17 @@ void launch_stream_epi(const SArgs &sa, int grid, hipStream_t stream) {
     hipLaunchKernelGGL((tgemm_stream<FWD, E, false>), dim3(grid), dim3(fs::kNT), 0, stream, sa);
 }
 
+// The epilogue's tile where the tiled kernel runs: the forward's, but 64 x 64
+// where 128 x 144 tiles would be one a CU at most.  Several small workgroups
+// then share a CU and end their tiles at different times: 2000x2000x2000 32 ->
+// 25 us, 8000x500x1020 28 -> 22, 16384x243x244 21 -> 15, 500x3000x2004 32 -> 20;
+// with more tiles the large ones win (8192x2304x1020: 60 against 74 us).
+int pick_tile_epi(const Shape &s, int64_t cus) {
+  const int t = pick_tile(s, cus);
+  const TileInfo &w = kTileInfo[TW];
+  return t == TW && ceil_div(s.R, w.bm) * ceil_div(s.Cc, w.bn) <= cus ? TS : t;
+}
+
 // what ternary_gemm_s8_epilogue adds to the scaled forward
 struct EpiArgs {
   const float *bias;
@@ -2937,7 +2948,7 @@ int run(int op, const int8_t *q, const void *p, void *out, int kind, const float
     o.act = ep->act;
   }
 
-  const int tile = pick_tile_for(op, s, mc.cus);
+  const int tile = ep ? pick_tile_epi(s, mc.cus) : pick_tile_for(op, s, mc.cus);
   const TileInfo &ti = kTileInfo[tile];
   Args a;
   a.q = q;
