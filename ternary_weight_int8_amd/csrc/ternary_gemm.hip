@@ -202,7 +202,7 @@ __device__ __forceinline__ void store1(void *base, int32_t kind, int64_t e, floa
     static_cast<uint16_t *>(base)[e] = __builtin_bit_cast(uint16_t, (__bf16)y);
 }
 
-// the epilogue of one element: bias, res and e as the caller fetched them
+// the epilogue of one element, and of four neighbours of a row
 template <int E>
 __device__ __forceinline__ void epi_put1(const Out &o, int64_t Cc, int64_t row, int64_t col, int32_t x, float r) {
 #pragma clang fp contract(off)   // every kernel rounds alike
@@ -246,15 +246,15 @@ __device__ __forceinline__ void epi_put4(const Out &o, int64_t Cc, int64_t row, 
 }
 
 // The epilogue of a wave's FM x FN fragments, four fragments of a row at a
-// time (more than the accumulators' own registers spilled).  Each pass is straight-line code; what depends on the
-// arguments (bias, Z, residual) is decided once a pass, not once an element:
-// with the decisions inside the unrolled elements, the code was over 100 KB
-// and ran 16384x3456x1280 with gelu in 120 us.  It takes 111 us now, 84 us
-// without activation and Z: 21 us a tile for the products as in the plain
+// time (a whole row of them spilled).  Each pass is straight-line code; what
+// depends on the arguments (bias, Z, residual) is decided once a pass, not once
+// an element: with the decisions inside the unrolled elements, the code was
+// over 100 KB and ran 16384x3456x1280 with gelu in 120 us.  It takes 111 us now,
+// 84 us without activation and Z: 21 us a tile for the products as in the plain
 // forward, and per wave and tile 144 elements of some 17 vector instructions,
 // which no MFMA covers, since the CU's waves reach their tiles' ends together.
-// Four fragments' lane moves issued ahead of the run before cost registers (spills, 117
-// us), and two workgroups of 256 x 144 a CU, which drift apart, 123 us.
+// Lane moves issued a run ahead spilled (117 us), and two workgroups of 256 x
+// 144 a CU, which drift apart, took 123 us.
 //   0  lanes: from the MFMA layout (lane l: row l % 16, columns 4 (l / 16) ..
 //      + 3) to four neighbouring lanes a row, by ds_bpermute.  float32: 16
 //      bytes a lane, 64 a row.  bfloat16: fragments in pairs, first exchanged
@@ -1914,10 +1914,11 @@ void tgemm_stream(SArgs a) {
 // order): after the awaited packed codes of step g + 2 come that batch's A loads
 // and D - 2 whole batches, after A(g + 2) the D - 2 batches.  Waves are WM x WN,
 // each TM x TN of the tile.
-// Bound by each step's chain (barrier, fragment reads, decode, barrier; about
-// 1000 cycles for 8 waves on 128 x 128, whose products take 256): without loads
-// and decode 16384x1280x3456 still takes 68 of 107 us, and neither whole-line A
-// loads nor A from the caches alone change it.  Measured beside it (4096x1280x3456
+// Bound by a step's LDS traffic and chain (barrier, fragment reads, decode,
+// barrier; about 1000 cycles for 8 waves on 128 x 128, whose products take 256):
+// without loads and decode 16384x1280x3456 still takes 68 of 107 us; whole-line A
+// loads, or A from the caches alone, change nothing, and half the barriers
+// little (36 against 44 us at best).  Measured beside it (4096x1280x3456
 // f32, 16384x1280x3456 bf16): 4 waves on 128 x 160 42 and 108 us, 8 on 128 x 160
 // 39 and 107, 4 on 64 x 160 42 and 148, 8 on 256 x 128 45 and 108, this 43 and
 // 107; at 2000x2048x2048, where tiles are few, 32, 27, 29, 29 and 20.
