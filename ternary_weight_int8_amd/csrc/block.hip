@@ -549,7 +549,8 @@ __global__ __launch_bounds__(max_t(W, V)) void norm_bwd_reg(NormBwdArgs a) {
         for (int i = 0; i < U; ++i) {
           const float g = d[i] * (f[i] * rstd);
           acc[j][i] += g;
-          part_sum = __builtin_fmaf(g, (j == un.last && i < un.dup) ? 0.f : gain[i], part_sum);
+          // left out by not adding it: a zero factor would make an infinity a NaN
+          part_sum = (j == un.last && i < un.dup) ? part_sum : __builtin_fmaf(g, gain[i], part_sum);
         }
         sum += part_sum;
       }

@@ -1,0 +1,50 @@
+"""Infinities and values near the ends of the range in the operators around
+the product, at widths that are not whole vectors."""
+import pytest
+
+from ternary_weight_int8_amd import binding as B
+
+torch = pytest.importorskip("torch")
+import block_ref as ref  # noqa: E402
+from test_gpu_block import DEV, KINDS, gen, normal, say  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def same_kind_of_values(got, want, what):
+    """NaN where the formula has NaN, an infinity of its sign where it has one, finite elsewhere."""
+    got, want = got.double(), want.double()
+    bad = (torch.isnan(got) != torch.isnan(want)) | (torch.isinf(got) != torch.isinf(want)) | (
+        torch.isinf(want) & (got.sign() != want.sign()))
+    if bool(bad.any()):
+        i = tuple(int(v) for v in bad.nonzero()[0])
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} are of another kind, first at {i}: {float(got[i])} for {float(want[i])}")
+
+
+# a wave a row; a workgroup a row with one unit a thread and with more; the
+# looped kernels.  9 columns from the end hold every place of a row's last two
+# vectors, of which the last may overlap the one before.
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("C", [9, 243, 509, 1282, 3461, 8197, 16379, 16401])
+def test_norm_backward_infinities(C, kind):
+    say(f"norm backward infinities {C} {kind}")
+    dt, g, n = KINDS[kind], gen(C, kind, 21), 9
+    H, dY = normal(g, n + 3, C, dtype=dt), normal(g, n + 3, C, dtype=dt, scale=1e-2)
+    H[H.abs() < 0.01] = 0.5                    # no 0 x infinity from a value that a type rounds to 0
+    gain = 1 + 0.1 * torch.rand(C, generator=g, device=DEV)
+    rstd = (H.double().square().mean(1) + 1e-5).rsqrt().float()
+    clean = B.ternary_rmsnorm_backward(dY, H, gain, rstd)
+    for i in range(n):
+        dY[i, C - 1 - i] = float("inf") if i % 2 else -float("inf")
+    dX, dgain = B.ternary_rmsnorm_backward(dY, H, gain, rstd)
+    dx, _, dg, _ = ref.norm_backward(dY.double(), H.double(), gain.double(), rstd.double(), None)
+    same_kind_of_values(dX, dx, "dX")
+    same_kind_of_values(dgain, dg, "dgain")
+    assert torch.equal(dX[n:], clean[0][n:]) and torch.equal(dgain[:C - n], clean[1][:C - n])
+    H[n, C - 2] = float("inf")                 # its rstd is 0: the product is NaN, and so is the row's sum
+    rstd[n] = 0
+    dX, dgain = B.ternary_rmsnorm_backward(dY, H, gain, rstd)
+    dx, _, dg, _ = ref.norm_backward(dY.double(), H.double(), gain.double(), rstd.double(), None)
+    same_kind_of_values(dX, dx, "dX")
+    same_kind_of_values(dgain, dg, "dgain")
+    assert torch.equal(dX[n + 1:], clean[0][n + 1:])
