@@ -640,9 +640,13 @@ __device__ __forceinline__ float back_sigm(float dy, float z, const Sigm &k) {
   return z == z ? d : z;   // the clamp drops a NaN
 }
 
-// relu2's 2 z is taken as (2 dy) z, which stays finite where the product does
+// relu2's 2 z dy is taken as p + p, p = z dy, which overflows only where the
+// product does (2 z or 2 dy alone may do so before); a NaN z stays one
 __device__ __forceinline__ float back_relu(float dy, float z) { return dy * (z > 0.f ? 1.f : (z == z ? 0.f : z)); }
-__device__ __forceinline__ float back_relu2(float dy, float z) { return (dy + dy) * (z < 0.f ? 0.f : z); }
+__device__ __forceinline__ float back_relu2(float dy, float z) {
+  const float p = dy * (z < 0.f ? 0.f : z);
+  return p + p;
+}
 __host__ __device__ __forceinline__ bool is_sigm(int act) { return act >= TGEMM_ACT_SILU; }
 static_assert(TGEMM_ACT_GELU_TANH > TGEMM_ACT_SILU && TGEMM_ACT_RELU2 < TGEMM_ACT_SILU, "is_sigm");
 

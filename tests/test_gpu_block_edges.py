@@ -48,3 +48,28 @@ def test_norm_backward_infinities(C, kind):
     same_kind_of_values(dX, dx, "dX")
     same_kind_of_values(dgain, dg, "dgain")
     assert torch.equal(dX[n + 1:], clean[0][n + 1:])
+
+
+# relu2's slope 2 z is as large as the value: the product 2 z dy overflows only
+# where the formula's does.  A wave a row, a workgroup a row, the looped kernel.
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("C", [3, 16, 2051, 16401])
+def test_relu2_backward_of_large_gradients(C, kind):
+    say(f"relu2 backward of large gradients {C} {kind}")
+    dt = KINDS[kind]
+    top = 2.0e38                               # more than half the largest float32
+    z = torch.tensor([0.0, 0.1, 1e-3, -0.0, -1.0, 0.75, 3.0, 1e-30], device=DEV, dtype=dt)
+    dY = torch.full((z.numel(), C), 1.0, device=DEV, dtype=dt)
+    dY[:, -1], dY[:, 0] = top, -top
+    Z = z[:, None].repeat(1, C)
+    dZ, dbias, Q, s = B.ternary_epilogue_backward(dY, Z, act="relu2")
+    dz, e, _, _ = ref.epilogue_backward(dY.double(), Z.double(), "relu2")
+    over = dz.abs() > 3.4e38                   # 2 z dy for z of 3: past the type
+    assert bool((over.any(1) == (z == 3)).all())
+    ref.check(torch.where(over, 0, dZ.double()), torch.where(over, 0, dz), ref.rounded(dz, e, dt), "dZ")
+    assert torch.equal(dZ[over].double(), torch.where(dz[over] > 0, float("inf"), -float("inf")).double())
+    for r in range(z.numel()):
+        if bool(over[r].any()):
+            assert not bool(torch.isfinite(s[r])) and bool((Q[r] == 0).all())
+        else:
+            ref.check_int8(Q[r:r + 1], s[r:r + 1], dz[r:r + 1], e[r:r + 1], f"row {r}")
