@@ -390,8 +390,7 @@ const char *ternary_gemm_status_str(int status);
  * (the smallest power-of-two alignment of the input pointers, in bytes),
  * which kernel runs (TGEMM_KERNEL_*), and that kernel's threads and LDS bytes
  * per workgroup.  The plan is that of the calls without a workspace and
- * without an epilogue (ternary_gemm_s8_epilogue follows the forward's plan but
- * for mid-size outputs, which have a kernel of their own or smaller tiles).
+ * without an epilogue, which has ternary_gemm_epilogue_plan below.
  * Returns TGEMM_OK, or the status the real call would return for these
  * dimensions (pointer checks excepted).
  */
@@ -413,6 +412,11 @@ const char *ternary_gemm_status_str(int status);
                                   8-wave workgroup per 16, 32 or 64 output
                                   columns and all M rows, its waves splitting
                                   the contraction                             */
+#define TGEMM_KERNEL_RING 5    /* the forward with its epilogue on mid-size
+                                  outputs (K % 64 == 0, 16-byte aligned A,
+                                  4-byte aligned Wpacked, 32-bit offsets): one
+                                  8-wave workgroup per 128 x 128 output tile,
+                                  operands loaded straight into LDS          */
 
 typedef struct tgemm_plan {
     int64_t out_rows, out_cols, contraction;
@@ -441,6 +445,14 @@ int ternary_gemm_plan(int op, int64_t M, int64_t N, int64_t K, int64_t align,
 int ternary_gemm_plan_on(int op, int64_t M, int64_t N, int64_t K, int64_t align,
                          int32_t cus, int32_t xcds, tgemm_plan *plan);
 int ternary_gemm_machine(int32_t *cus, int32_t *xcds);
+
+/*
+ * The plan of ternary_gemm_s8_epilogue, for a machine of cus compute units in
+ * xcds XCDs (256 and 8 on MI355X): the forward's kernels, and
+ * TGEMM_KERNEL_RING.
+ */
+int ternary_gemm_epilogue_plan(int64_t M, int64_t N, int64_t K, int64_t align, int32_t cus, int32_t xcds,
+                               tgemm_plan *plan);
 
 /*
  * Output tile that workgroup `workgroup` computes in its iteration

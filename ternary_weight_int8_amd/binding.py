@@ -48,6 +48,7 @@ EXPORTS = (
     "ternary_epilogue_backward_workspace",
     "ternary_clip_grad_norm",
     "ternary_clip_grad_norm_workspace",
+    "ternary_gemm_epilogue_plan",
 )
 
 OPS = {"fwd": 0, "dx": 1, "dw": 2}
@@ -67,7 +68,7 @@ class TgemmPlan(ctypes.Structure):
     ]
 
 
-KERNEL_TILED, KERNEL_SPLIT, KERNEL_STREAM, KERNEL_SKINNY = 0, 2, 3, 4   # TgemmPlan.kernel
+KERNEL_TILED, KERNEL_SPLIT, KERNEL_STREAM, KERNEL_SKINNY, KERNEL_RING = 0, 2, 3, 4, 5   # TgemmPlan.kernel
 
 
 class TernaryGemmError(RuntimeError):
@@ -134,7 +135,8 @@ def lib():
                 ("ternary_epilogue_backward", [p, p, i32, i32, p, p, p, p, i64, i64, p, i64, p]),
                 ("ternary_epilogue_backward_workspace", [i64, i64, pi64]),
                 ("ternary_clip_grad_norm", [p, p, p, p, i64, f32, f32, p, p, i64, p]),
-                ("ternary_clip_grad_norm_workspace", [p, i64, pi64])):
+                ("ternary_clip_grad_norm_workspace", [p, i64, pi64]),
+                ("ternary_gemm_epilogue_plan", [i64, i64, i64, i64, i32, i32, ctypes.POINTER(TgemmPlan)])):
             f = getattr(L, name)
             f.argtypes = args
             f.restype = ctypes.c_int
@@ -185,6 +187,14 @@ def plan(op: str, M: int, N: int, K: int, align: int = 256, cus: int = None, xcd
         st = lib().ternary_gemm_plan_on(OPS[op], M, N, K, align, cus, xcds, ctypes.byref(pl))
     if st != OK:
         raise TernaryGemmError("ternary_gemm_plan", st, status_str(st))
+    return pl
+
+
+def epilogue_plan(M: int, N: int, K: int, align: int = 256, cus: int = 256, xcds: int = 8):
+    """The launch plan of ternary_gemm_s8_epilogue, for MI355X unless cus and xcds name another machine."""
+    pl = TgemmPlan()
+    _done("ternary_gemm_epilogue_plan",
+          lib().ternary_gemm_epilogue_plan(M, N, K, align, cus, xcds, ctypes.byref(pl)))
     return pl
 
 

@@ -2634,7 +2634,7 @@ hipError_t launch_f(const Args &a, bool fast, hipStream_t stream) {
 // (A variant that loads the int8 operand of the forward and dX straight into
 // MFMA registers, without LDS, measured no faster in the three-product step
 // on MI355X and was left out.)
-enum KernelId { KTILED = 0, KSPLIT = 2, KSTREAM = 3, KSKINNY = 4 };
+enum KernelId { KTILED = 0, KSPLIT = 2, KSTREAM = 3, KSKINNY = 4, KRING = 5 };
 
 // The machine the plans are made for: compute units (one persistent
 // workgroup each) and XCDs (workgroup b runs on XCD b % xcds, each XCD with
@@ -2848,8 +2848,9 @@ typedef rg::Cfg<128, 128, 4, 2, 4> Ring;
 // tiles where they fill the chip exactly, two a CU (4096x4096x4096: 80 against
 // 90 us).
 bool filled(int64_t tiles, int64_t slots) { return 4 * tiles >= 3 * ceil_div(tiles, slots) * slots; }
-bool ring_ok(int64_t M, int64_t N, int64_t K, const void *A, const void *W, const StreamPlan &sp, const Machine &mc) {
-  if (K % BK != 0 || !aligned(A, 16) || !aligned(W, 4) || M > INT32_MAX / K || N > INT32_MAX / (K / 4)) return false;
+bool ring_ok(int64_t M, int64_t N, int64_t K, uintptr_t qalign, uintptr_t walign, const StreamPlan &sp,
+             const Machine &mc) {
+  if (K % BK != 0 || qalign % 16 != 0 || walign % 4 != 0 || M > INT32_MAX / K || N > INT32_MAX / (K / 4)) return false;
   const int64_t tiles = ceil_div(M, Ring::BM) * ceil_div(N, Ring::BN);
   const int64_t large = ceil_div(M, TileShapes::L::BM) * ceil_div(N, TileShapes::L::BN);
   if (tiles > INT32_MAX || 4 * tiles < 3 * mc.cus) return false;
@@ -3041,7 +3042,7 @@ int run(int op, const int8_t *q, const void *p, void *out, int kind, const float
   }
   {
     const StreamPlan sp = stream_plan(op, M, N, K, align_of(q), align_of(p), mc);
-    const bool ring = epi != EPI_NONE && ring_ok(M, N, K, q, p, sp, mc);
+    const bool ring = epi != EPI_NONE && ring_ok(M, N, K, align_of(q), align_of(p), sp, mc);
     if (sp.ok || ring) {
       SArgs sa;
       sa.xcds = mc.xcds;
@@ -3111,6 +3112,79 @@ int scratch_of(void **out) {
     if (dev < kMaxDev) cache[dev].store(ptr, std::memory_order_release);
   }
   *out = ptr;
+  return TGEMM_OK;
+}
+
+// the plan of a call, with an epilogue or without, in the order in which run() chooses
+int fill_plan(int op, bool epi, int64_t M, int64_t N, int64_t K, int64_t align, int32_t cus, int32_t xcds,
+              tgemm_plan *plan) {
+  if (!plan) return TGEMM_ERR_NULL;
+  const Machine mc = {cus, xcds};
+  if (!machine_ok(mc)) return TGEMM_ERR_DIM;
+  const int st = check_dims(op, M, N, K);
+  if (st != TGEMM_OK) return st;
+  const Shape s = shape_of(op, M, N, K);
+  const uintptr_t al = align > 0 ? (uintptr_t)align : 1;
+  memset(plan, 0, sizeof(*plan));
+  plan->out_rows = s.R;
+  plan->out_cols = s.Cc;
+  plan->contraction = s.L;
+  plan->fast_path = fast_ok(op, M, N, K, al, al) ? 1 : 0;
+  plan->xcds = mc.xcds;
+  {
+    SkinnyPlan kp = skinny_plan(op, M, N, K, al, al, mc);
+    if (!kp.ok) kp = skinny_dx_plan(op, M, N, K, al, al, mc);
+    if (kp.ok) {
+      plan->tile_rows = 16 * kp.mf;
+      plan->tile_cols = 16 * kp.nb;
+      plan->tiles = kp.grid;
+      plan->workgroups = kp.grid;
+      plan->tiles_per_workgroup = 1;
+      plan->band_cols = kp.grid;
+      plan->kernel = KSKINNY;
+      plan->threads_per_workgroup = sk::kNT;
+      plan->lds_bytes = kp.lds;
+      return TGEMM_OK;
+    }
+  }
+  {
+    const StreamPlan sp = stream_plan(op, M, N, K, al, al, mc);
+    if (epi && ring_ok(M, N, K, al, al, sp, mc)) {
+      plan->tile_rows = Ring::BM;
+      plan->tile_cols = Ring::BN;
+      plan->band_cols = (int32_t)ceil_div(N, Ring::BN);
+      plan->tiles = ceil_div(M, Ring::BM) * plan->band_cols;
+      plan->workgroups = plan->tiles;
+      plan->tiles_per_workgroup = 1;
+      plan->kernel = KRING;
+      plan->threads_per_workgroup = Ring::NT;
+      plan->lds_bytes = Ring::kLds;
+      return TGEMM_OK;
+    }
+    if (sp.ok) {
+      plan->tile_rows = fs::BM;
+      plan->tile_cols = sp.bn;
+      plan->tiles = sp.tiles;
+      plan->workgroups = sp.grid;
+      plan->tiles_per_workgroup = ceil_div(ceil_div(sp.tiles, mc.xcds), sp.grid / mc.xcds);
+      plan->band_cols = sp.tiles_c;
+      plan->kernel = KSTREAM;
+      plan->threads_per_workgroup = fs::kNT;
+      plan->lds_bytes = sp.lds + fs::BM * 4;   // stages + the tile's row scales
+      return TGEMM_OK;
+    }
+  }
+  const int tile = epi ? pick_tile_epi(s, mc.cus) : pick_tile_for(op, s, mc.cus);
+  const TileInfo &ti = kTileInfo[tile];
+  plan->tile_rows = ti.bm;
+  plan->tile_cols = ti.bn;
+  plan->tiles = ceil_div(s.R, ti.bm) * ceil_div(s.Cc, ti.bn);
+  plan->workgroups = plan->tiles;
+  plan->tiles_per_workgroup = 1;
+  plan->band_cols = pick_band_cols(op, M, N, K, (int32_t)ceil_div(s.Cc, ti.bn), mc.xcds);
+  plan->kernel = pick_kernel(op, tile, s.L, plan->tiles, mc);
+  plan->threads_per_workgroup = plan->kernel == KSPLIT ? 2 * kThreads : kThreads;
+  plan->lds_bytes = kernel_lds(op, plan->kernel, tile);
   return TGEMM_OK;
 }
 
@@ -3245,62 +3319,12 @@ int ternary_gemm_machine(int32_t *cus, int32_t *xcds) {
 
 int ternary_gemm_plan_on(int op, int64_t M, int64_t N, int64_t K, int64_t align, int32_t cus, int32_t xcds,
                          tgemm_plan *plan) {
-  if (!plan) return TGEMM_ERR_NULL;
-  const Machine mc = {cus, xcds};
-  if (!machine_ok(mc)) return TGEMM_ERR_DIM;
-  const int st = check_dims(op, M, N, K);
-  if (st != TGEMM_OK) return st;
-  const Shape s = shape_of(op, M, N, K);
-  const uintptr_t al = align > 0 ? (uintptr_t)align : 1;
-  memset(plan, 0, sizeof(*plan));
-  plan->out_rows = s.R;
-  plan->out_cols = s.Cc;
-  plan->contraction = s.L;
-  plan->fast_path = fast_ok(op, M, N, K, al, al) ? 1 : 0;
-  plan->xcds = mc.xcds;
-  {
-    SkinnyPlan kp = skinny_plan(op, M, N, K, al, al, mc);
-    if (!kp.ok) kp = skinny_dx_plan(op, M, N, K, al, al, mc);
-    if (kp.ok) {
-      plan->tile_rows = 16 * kp.mf;
-      plan->tile_cols = 16 * kp.nb;
-      plan->tiles = kp.grid;
-      plan->workgroups = kp.grid;
-      plan->tiles_per_workgroup = 1;
-      plan->band_cols = kp.grid;
-      plan->kernel = KSKINNY;
-      plan->threads_per_workgroup = sk::kNT;
-      plan->lds_bytes = kp.lds;
-      return TGEMM_OK;
-    }
-  }
-  {
-    const StreamPlan sp = stream_plan(op, M, N, K, al, al, mc);
-    if (sp.ok) {
-      plan->tile_rows = fs::BM;
-      plan->tile_cols = sp.bn;
-      plan->tiles = sp.tiles;
-      plan->workgroups = sp.grid;
-      plan->tiles_per_workgroup = ceil_div(ceil_div(sp.tiles, mc.xcds), sp.grid / mc.xcds);
-      plan->band_cols = sp.tiles_c;
-      plan->kernel = KSTREAM;
-      plan->threads_per_workgroup = fs::kNT;
-      plan->lds_bytes = sp.lds + fs::BM * 4;   // stages + the tile's row scales
-      return TGEMM_OK;
-    }
-  }
-  const int tile = pick_tile_for(op, s, mc.cus);
-  const TileInfo &ti = kTileInfo[tile];
-  plan->tile_rows = ti.bm;
-  plan->tile_cols = ti.bn;
-  plan->tiles = ceil_div(s.R, ti.bm) * ceil_div(s.Cc, ti.bn);
-  plan->workgroups = plan->tiles;
-  plan->tiles_per_workgroup = 1;
-  plan->band_cols = pick_band_cols(op, M, N, K, (int32_t)ceil_div(s.Cc, ti.bn), mc.xcds);
-  plan->kernel = pick_kernel(op, tile, s.L, plan->tiles, mc);
-  plan->threads_per_workgroup = plan->kernel == KSPLIT ? 2 * kThreads : kThreads;
-  plan->lds_bytes = kernel_lds(op, plan->kernel, tile);
-  return TGEMM_OK;
+  return fill_plan(op, false, M, N, K, align, cus, xcds, plan);
+}
+
+int ternary_gemm_epilogue_plan(int64_t M, int64_t N, int64_t K, int64_t align, int32_t cus, int32_t xcds,
+                               tgemm_plan *plan) {
+  return fill_plan(FWD, true, M, N, K, align, cus, xcds, plan);
 }
 
 int ternary_gemm_plan(int op, int64_t M, int64_t N, int64_t K, int64_t align, tgemm_plan *plan) {

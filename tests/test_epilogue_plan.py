@@ -1,0 +1,53 @@
+"""Which kernel the product with its epilogue takes, by the host-only plan query."""
+import ctypes
+
+import pytest
+
+from shapes import TILES
+from ternary_weight_int8_amd import binding as B
+
+
+def test_refusals():
+    pl = B.TgemmPlan()
+    q = B.lib().ternary_gemm_epilogue_plan
+    assert q(4, 8, 16, 256, 256, 8, None) == B.ERR_NULL
+    p = ctypes.byref(pl)
+    for M, N, K in ((0, 8, 16), (4, 0, 16), (4, 8, 0)):
+        assert q(M, N, K, 256, 256, 8, p) == B.ERR_DIM
+    assert q(4, 8, 18, 256, 256, 8, p) == B.ERR_PACK
+    assert q(4, 8, 1 << 24, 256, 256, 8, p) == B.ERR_BOUND
+    for cus, xcds in ((0, 8), (256, 0), (100, 8)):
+        assert q(4, 8, 16, 256, cus, xcds, p) == B.ERR_DIM
+
+
+def test_kernel_choice():
+    k = lambda *s, **kw: B.epilogue_plan(*s, **kw).kernel  # noqa: E731
+    tile = lambda *s, **kw: (B.epilogue_plan(*s, **kw).tile_rows, B.epilogue_plan(*s, **kw).tile_cols)  # noqa: E731
+    assert k(1, 3456, 1280) == k(32, 64, 64) == B.KERNEL_SKINNY
+    assert k(33, 3456, 1280) == k(32, 64, 80) == B.KERNEL_TILED
+    assert k(16384, 3456, 1280) == B.KERNEL_STREAM                 # 768 tiles of 512 x 144
+    assert k(16384, 1280, 3456) == B.KERNEL_RING                   # 288 of them: a second round for 32
+    assert k(4096, 1280, 3456) == B.KERNEL_RING
+    assert k(4096, 1280, 3456, align=8) == k(4096, 1280, 3452) == B.KERNEL_TILED
+    assert k(1000, 1000, 1024) == B.KERNEL_TILED                   # 64 tiles of 128 x 128
+    assert k(2000, 2048, 2048) == B.KERNEL_RING                    # 256
+    assert k(4096, 4096, 4096) == B.KERNEL_TILED                   # 512 tiles of 256 x 128
+    assert tile(2000, 2000, 2000) == (64, 64)                      # at most one 128 x 144 tile a CU
+    assert tile(8192, 2304, 1020) == (128, 144)
+    assert tile(4096, 4096, 1020) == (256, 128)
+    # without an epilogue none takes the ring kernel, and the forward's own plan stands
+    assert B.plan("fwd", 4096, 1280, 3456).kernel == B.KERNEL_TILED
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 17, 64), (4096, 1280, 3456), (3001, 1250, 1088), (16384, 1280, 128),
+                                   (15001, 2301, 128), (8191, 2301, 68), (2000, 2000, 2000)])
+@pytest.mark.parametrize("cus,xcds", [(256, 8), (64, 2)])
+def test_every_output_tile_covered_once(M, N, K, cus, xcds):
+    pl = B.epilogue_plan(M, N, K, cus=cus, xcds=xcds)
+    seen = [t for wg in range(pl.workgroups) for it in range(pl.tiles_per_workgroup)
+            if (t := B.tile_of(pl, wg, it)) is not None]
+    want = {(r, c) for r in range(0, M, pl.tile_rows) for c in range(0, N, pl.tile_cols)}
+    assert len(seen) == len(want) == pl.tiles and set(seen) == want
+    assert pl.lds_bytes <= 160 * 1024 and pl.threads_per_workgroup in (256, 512)
+    if pl.kernel == B.KERNEL_TILED:
+        assert (pl.tile_rows, pl.tile_cols) in TILES
