@@ -51,3 +51,36 @@ def test_every_output_tile_covered_once(M, N, K, cus, xcds):
     assert pl.lds_bytes <= 160 * 1024 and pl.threads_per_workgroup in (256, 512)
     if pl.kernel == B.KERNEL_TILED:
         assert (pl.tile_rows, pl.tile_cols) in TILES
+
+
+def gpu_shapes():
+    """(M, N, K, alignment of the operands) of every product that the GPU tests of the epilogue run."""
+    pytest.importorskip("torch")
+    import test_gpu_block as block
+    import test_gpu_epilogue_kernels as kernels
+
+    def of(f):
+        return next(m.args[1] for m in f.pytestmark if m.name == "parametrize" and m.args[0].startswith("M,N,K"))
+
+    shapes = [(*s, 256) for s in block.PRODUCTS + kernels.TILED + kernels.FEW_ROWS + of(block.test_product_epilogue_large)]
+    for M, N, K, offset in of(block.test_product_epilogue_misaligned):
+        shapes += [(M, N, K, 256), (M, N, K, offset & -offset)]
+    return shapes
+
+
+def test_gpu_tests_reach_every_choice():
+    seen, ragged = set(), set()
+    for M, N, K, align in gpu_shapes():
+        pl = B.epilogue_plan(M, N, K, align=align)
+        choice = (pl.kernel, pl.tile_rows, pl.tile_cols, M > 8 if pl.kernel == B.KERNEL_SKINNY else pl.fast_path)
+        seen.add(choice)
+        ragged.add((*choice, M % pl.tile_rows != 0 or N % pl.tile_cols != 0))
+    want = {(B.KERNEL_TILED, *t, fast) for t in TILES for fast in (0, 1)}
+    want |= {(B.KERNEL_SKINNY, 16, c, al) for c in (16, 32, 64) for al in (False, True)}
+    want |= {(B.KERNEL_SKINNY, 32, c, True) for c in (16, 32, 64)}
+    want |= {(B.KERNEL_STREAM, 512, 144, 1), (B.KERNEL_RING, 128, 128, 1)}
+    assert seen == want, (want - seen, seen - want)
+    # the tiles' guarded and unguarded ends
+    for c in want:
+        if c[0] != B.KERNEL_SKINNY and c[3]:
+            assert (*c, True) in ragged and (*c, False) in ragged, c
