@@ -2839,22 +2839,35 @@ hipError_t launch_op(const Args &a, int kernel, int tile, bool fast, hipStream_t
 typedef rg::Cfg<128, 128, 4, 2, 4> Ring;
 
 // Whether the epilogue's forward runs the ring kernel: the stream kernel's
-// alignment and 32-bit offsets, and tiles for three quarters of the CUs at
-// least (fewer 128 x 128 tiles leave more idle than 64 x 64 ones of the tiled
-// kernel: 1000x1000x1024 14 against 12 us, 8000x500x1024 16 against 24 us).
-// The persistent stream kernel stays ahead where its 512 x 144 tiles fill its
-// rounds (16384x3456x1280 with gelu: 111 against 132 us; at 16384x1280x3456, 288
-// tiles for 256 CUs, 146 against 107 us), and so do the tiled kernel's 256 x 128
-// tiles where they fill the chip exactly, two a CU (4096x4096x4096: 80 against
-// 90 us).
+// alignment and 32-bit offsets, and
+//   - tiles for three quarters of the CUs at least: fewer 128 x 128 tiles leave
+//     more idle than 64 x 64 ones of the tiled kernel (1000x1000x1024 14 against
+//     12 us, 1500x2048x2048, 192 tiles, 16.5 against 16.0, 2000x2048x2048, 256 tiles,
+//     16.7 against 19.4, 8000x500x1024 16 against 24 us);
+//   - where there are stream tiles for every CU, that they leave more than a
+//     quarter of the stream kernel's rounds empty (16384 rows, bf16, ring against
+//     stream: K = 1024, 288 tiles 40 against 54 us, 320 46 against 48, 352 52
+//     against 51, 384 56 against 53, 448 63 against 55, 512 74 against 58, 544 78
+//     against 77, 608 84 against 79; K = 3456, 288 tiles 100 against 122, 352 131
+//     against 127, 384 135 against 128; 16384x3456x1280 with gelu 125 against 108);
+//   - else, that a CU has one, two, three or five tiles, or four of at most 8 steps.
+//     A 256 x 128 tile of the tiled kernel takes 1.65 times as long as one of
+//     these, so it loses where half of its last round is empty and wins with four
+//     (bf16, ring against tiled, K = 4096 and 1024: two tiles a CU 43 against 46
+//     and 16 against 20 us, three 68 against 70 and 24 against 28, four, from
+//     4096x3200 to 4096x4096, 80-84 against 69-73 and 28-29 against 27-28, five,
+//     4096x4224, 101 against 99 and 34 against 39; at 50000x288x1024 41 against 43),
+//     but its longer start shows in few steps (four tiles: 4096x4096x64 14 against
+//     16 us, 8192x2048x256 16.3 against 17.2, 4096x4096x512 21.1 against 21.8).  Six
+//     and more occur only where the last of these columns is mostly past the
+//     output (65000x288x1024 52 against 50 us, 100000x144x1024 55 against 50).
 bool filled(int64_t tiles, int64_t slots) { return 4 * tiles >= 3 * ceil_div(tiles, slots) * slots; }
 bool ring_ok(int64_t M, int64_t N, int64_t K, uintptr_t qalign, uintptr_t walign, const StreamPlan &sp,
              const Machine &mc) {
   if (K % BK != 0 || qalign % 16 != 0 || walign % 4 != 0 || M > INT32_MAX / K || N > INT32_MAX / (K / 4)) return false;
-  const int64_t tiles = ceil_div(M, Ring::BM) * ceil_div(N, Ring::BN);
-  const int64_t large = ceil_div(M, TileShapes::L::BM) * ceil_div(N, TileShapes::L::BN);
+  const int64_t tiles = ceil_div(M, Ring::BM) * ceil_div(N, Ring::BN), a_cu = ceil_div(tiles, mc.cus);
   if (tiles > INT32_MAX || 4 * tiles < 3 * mc.cus) return false;
-  return sp.ok ? !filled(sp.tiles, sp.grid) : large % (2 * mc.cus) != 0;
+  return sp.ok ? !filled(sp.tiles, sp.grid) : a_cu <= (K <= 8 * BK ? 4 : 3) || a_cu == 5;
 }
 
 template <int E>

@@ -62,7 +62,7 @@ def gpu_shapes():
     def of(f):
         return next(m.args[1] for m in f.pytestmark if m.name == "parametrize" and m.args[0].startswith("M,N,K"))
 
-    shapes = [(*s, 256) for s in block.PRODUCTS + kernels.TILED + kernels.FEW_ROWS + of(block.test_product_epilogue_large)]
+    shapes = [(*s, 256) for s in block.PRODUCTS + kernels.TILED + kernels.RING + kernels.FEW_ROWS + of(block.test_product_epilogue_large)]
     for M, N, K, offset in of(block.test_product_epilogue_misaligned):
         shapes += [(M, N, K, 256), (M, N, K, offset & -offset)]
     return shapes
@@ -84,3 +84,23 @@ def test_gpu_tests_reach_every_choice():
     for c in want:
         if c[0] != B.KERNEL_SKINNY and c[3]:
             assert (*c, True) in ragged and (*c, False) in ragged, c
+
+
+# 256 x 128 tiles of the tiled kernel that fill a CU's last round beat the ring
+# kernel's 128 x 128 ones over many steps, at every size where they do and not at one
+@pytest.mark.parametrize("K", [64, 512, 576, 1024, 4096])
+@pytest.mark.parametrize("M,N,a_cu", [
+    (2000, 2048, 1), (4096, 1536, 2), (4096, 2048, 2), (4096, 2176, 3), (2816, 4096, 3), (6144, 2048, 3), (4096, 3200, 4),
+    (4096, 3584, 4), (4096, 3968, 4), (4096, 4096, 4), (4095, 4095, 4), (8192, 1920, 4), (4096, 4224, 5), (4096, 4352, 5),
+    (50000, 288, 5), (65000, 288, 6), (100000, 144, 7)])
+def test_ring_kernel_by_the_tiles_of_a_cu(M, N, a_cu, K):
+    assert -(-(-(-M // 128) * -(-N // 128)) // 256) == a_cu
+    assert B.plan("fwd", M, N, K).kernel != B.KERNEL_STREAM
+    assert (B.epilogue_plan(M, N, K).kernel == B.KERNEL_RING) == (a_cu in (1, 2, 3, 5) or (a_cu == 4 and K <= 512))
+
+
+def test_ring_kernel_where_the_stream_kernel_would_idle():
+    for tiles, ring in ((288, True), (352, True), (384, False), (448, False), (512, False), (544, True), (608, False)):
+        N = 144 * tiles // 32                                    # 16384 rows: 32 of 512
+        assert B.plan("fwd", 16384, N, 1024).kernel == B.KERNEL_STREAM and B.plan("fwd", 16384, N, 1024).tiles == tiles
+        assert (B.epilogue_plan(16384, N, 1024).kernel == B.KERNEL_RING) == ring, tiles

@@ -17,11 +17,13 @@ pytestmark = pytest.mark.gpu
 # with K % 16 == 0 (vector loads), then with rows of 4-byte pieces
 TILED = [(8192, 2304, 80), (8191, 2301, 80), (8191, 2301, 68), (4096, 4096, 80), (4095, 4093, 80), (4096, 4096, 68),
          (4095, 4093, 336), (4095, 4091, 148), (640, 704, 80), (1990, 2000, 144), (500, 1777, 404)]
+# the kernel of mid-size outputs with its last columns mostly past the output, and five tiles a CU
+RING = [(16384, 243, 256), (4101, 4224, 128)]
 FEW_ROWS = [(1, 4100, 128), (7, 8200, 128), (12, 4100, 64), (16, 8207, 192), (20, 4100, 128), (32, 4099, 1024)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("M,N,K", TILED + FEW_ROWS)
+@pytest.mark.parametrize("M,N,K", TILED + RING + FEW_ROWS)
 def test_product_epilogue_in_every_kernel(M, N, K, kind):
     pl = B.epilogue_plan(M, N, K)
     say(f"product epilogue {M}x{N}x{K} {kind}: kernel {pl.kernel}, tile {pl.tile_rows}x{pl.tile_cols}, fast {pl.fast_path}")
