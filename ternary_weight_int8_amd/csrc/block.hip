@@ -1022,8 +1022,15 @@ void launch_finish(const float *P, float *out, int64_t rows, int64_t C, hipStrea
 // bf16: 33.6 us, 37.6 with a workgroup a row; its backward pass 46.9 us against
 // 38.1); else a workgroup of as many waves as the row fills with the
 // fewest units a thread (3456 bf16: 432 units, 7 waves of one, 4% idle lanes;
-// four waves of two leave 16% idle).  For the backward passes (`sums`), few
-// short rows go to one workgroup, whose column sums need no second launch.
+// four waves of two leave 16% idle).  For the backward passes (`sums`), at most
+// 32 rows of one unit a lane go to one workgroup, whose column sums need no
+// workspace and no second launch.  That costs the GPU more from 12 rows on, since the
+// workgroup's waves add into LDS one after another (norm, 243 f32, in a graph:
+// 8 rows 3.8 against 5.0 us, 12 rows 4.9 and 4.9, 27 rows 6.4 and 5.2; epilogue,
+// 512 bf16: 8.2 and 6.0 at 12 rows, 11.8 and 6.3 at 27), but it saves the host
+// more than that (norm, 243 f32, calls one after another: 10.4 against 15.0 us),
+// up to where the GPU takes as long as the host (64 rows: 7.8 us for the norm of
+// 243 f32, 16.4 against 14.4 for the epilogue of 512 bf16).
 // v 0: the looped kernels.
 struct RowPlan {
   int w, v, bt;
@@ -1037,7 +1044,8 @@ RowPlan row_plan(int64_t R, int64_t C, int kind, bool sums) {
   p.w = nu <= 64 || (nu <= 256 && R >= 1024 && !sums) ? 1 : 0;
   p.v = (int)ceil_div(nu, p.w ? 64 : 1024);
   p.bt = p.w ? 256 : 64 * (int)ceil_div(nu, 64 * p.v);
-  if (sums && nu <= 64 && R <= 64) p.bt = 64 * (int)(R < 16 ? R : 16);
+  const bool one = sums && nu <= 64 && R <= 32;
+  if (one) p.bt = 64 * (int)(R < 16 ? R : 16);
   const int64_t groups = ceil_div(R, p.w ? p.bt / 64 : 1), per_cu = 64 * (sums ? kBwdWaves : kNormWaves) / p.bt;
   int64_t cap = kCUs * (per_cu > 1 ? per_cu : 1);
   // column sums: at least four rows a workgroup, down to two workgroups a CU (a
@@ -1045,7 +1053,7 @@ RowPlan row_plan(int64_t R, int64_t C, int kind, bool sums) {
   // 512 12.1 us)
   const int64_t least = R / 4 > 2 * kCUs ? R / 4 : 2 * kCUs;
   if (sums && cap > least) cap = least;
-  p.grid = sums && nu <= 64 && R <= 64 ? 1 : groups < cap ? groups : cap;
+  p.grid = one ? 1 : groups < cap ? groups : cap;
   return p;
 }
 

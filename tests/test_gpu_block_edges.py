@@ -73,3 +73,25 @@ def test_relu2_backward_of_large_gradients(C, kind):
             assert not bool(torch.isfinite(s[r])) and bool((Q[r] == 0).all())
         else:
             ref.check_int8(Q[r:r + 1], s[r:r + 1], dz[r:r + 1], e[r:r + 1], f"row {r}")
+
+
+# one workgroup for every row, whose waves take up to two rows each, and the
+# first size past it
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("C", [9, 243, 256, 512])
+@pytest.mark.parametrize("R", [2, 15, 16, 17, 31, 32, 33])
+def test_backward_of_few_short_rows(R, C, kind):
+    say(f"backward of few short rows {R}x{C} {kind}")
+    dt, g = KINDS[kind], gen(R, C, kind, 23)
+    H, dY, Z = normal(g, R, C, dtype=dt), normal(g, R, C, dtype=dt, scale=1e-2), normal(g, R, C, dtype=dt, scale=2.0)
+    gain = 1 + normal(g, C, scale=0.1)
+    rstd = (H.double().square().mean(1) + 1e-5).rsqrt().float()
+    dX, dgain = B.ternary_rmsnorm_backward(dY, H, gain, rstd)
+    dx, e, dg, eg = ref.norm_backward(dY.double(), H.double(), gain.double(), rstd.double(), None)
+    ref.check(dX, dx, ref.rounded(dx, e, dt), "dX")
+    ref.check(dgain, dg, eg, "dgain")
+    dZ, dbias, Q, s = B.ternary_epilogue_backward(dY, Z, act="silu")
+    dz, e, db, eb = ref.epilogue_backward(dY.double(), Z.double(), "silu")
+    ref.check(dZ, dz, ref.rounded(dz, e, dt), "dZ")
+    ref.check(dbias, db, eb, "dbias")
+    ref.check_int8(Q, s, dz, e, "dZ")
