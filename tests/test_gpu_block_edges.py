@@ -1,5 +1,7 @@
 """Infinities and values near the ends of the range in the operators around
-the product, at widths that are not whole vectors."""
+the product, at widths that are not whole vectors; few short rows; int8 rows
+by IEEE division."""
+import numpy
 import pytest
 
 from ternary_weight_int8_amd import binding as B
@@ -95,3 +97,19 @@ def test_backward_of_few_short_rows(R, C, kind):
     ref.check(dZ, dz, ref.rounded(dz, e, dt), "dZ")
     ref.check(dbias, db, eb, "dbias")
     ref.check_int8(Q, s, dz, e, "dZ")
+
+
+# bfloat16 gradients without an activation often lie on the border between two
+# int8 values, where a scale one step off changes them: the scale and the
+# quotient are those of IEEE division, on a host
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("R,C", [(453, 601), (41, 192), (4079, 1353), (3, 16401)])
+def test_int8_rows_are_those_of_ieee_division(R, C, kind):
+    say(f"int8 rows by IEEE division {R}x{C} {kind}")
+    dY = normal(gen(R, C, kind, 25), R, C, dtype=KINDS[kind], scale=1e-3)
+    dZ, _, Q, s = B.ternary_epilogue_backward(dY, dY, act="none")
+    y = dY.float().cpu().numpy()
+    scale = abs(y).max(1) / numpy.float32(127)
+    assert scale.dtype == numpy.float32 and (s.cpu().numpy() == scale).all()
+    assert (Q.cpu().numpy() == numpy.clip(numpy.rint(y / scale[:, None]), -127, 127)).all()
+    assert torch.equal(dZ, dY)
