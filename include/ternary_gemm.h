@@ -265,7 +265,9 @@ int ternary_quantize_cols(const void *X, int in_kind, int8_t *Q, float *scale, i
  *     bit patterns by the call's kind (TGEMM_IN_*, TGEMM_OUT_*), any width,
  *     any alignment from the element's own;
  *   - sums and statistics are float32 (the global norm's double), summed in
- *     a fixed order without atomics: repeated calls give identical bits;
+ *     a fixed order without atomics: repeated calls give identical bits.  The
+ *     order goes by the sizes, so a row's rstd may differ in its last bits
+ *     between calls with other numbers of rows (the product's outputs do not);
  *   - int8 rows and their scales are what ternary_quantize_rows would make of
  *     the float32 values before they are rounded to the kind: s = max|y| / 127,
  *     q = clamp(rint(y / s), -127, 127), q = 0 where s is 0 or not finite.  The
@@ -365,8 +367,9 @@ int ternary_epilogue_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
  * in them are DEVICE pointers.  Gradient i has sizes[i] >= 0 elements
  * (pointers of an empty one are not used) of kinds[i] (TGEMM_IN_*), and
  * outs[i], of the same kind, may be grads[i] itself.  `norm` is a DEVICE
- * float.  A norm that is not finite is reported as it is and makes the factor
- * 0 or NaN, as the formula does.
+ * float, and the factor is computed from it as it is stored: a norm past the
+ * largest float32 is an infinity.  A norm that is not finite makes the factor 0
+ * or NaN, as the formula does.
  * Requires count >= 1 and every size >= 0 (TGEMM_ERR_DIM), max_norm >= 0 and
  * eps >= 0, neither a NaN (TGEMM_ERR_VALUE).
  */

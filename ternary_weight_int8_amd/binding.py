@@ -2,7 +2,9 @@
 
 Every product runs in the library's HIP kernels.  There is no fallback: if the
 library is missing or a call fails, these functions raise.  PyTorch supplies
-device memory and the current stream; the library never allocates.
+device memory and the current stream; the library never allocates.  A call
+launches on the current HIP device, which has to be its tensors' (one process a
+GPU).
 """
 from __future__ import annotations
 

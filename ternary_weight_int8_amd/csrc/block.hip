@@ -19,8 +19,11 @@
 
 #include "ternary_gemm.h"
 
-// sums and products are fused only where fma is written, so that every variant
-// of a kernel rounds alike
+// Sums and products are fused only where fma is written, so that a kernel
+// rounds alike whatever its widths are compiled for.  The kernels of other row
+// lengths and counts add a row, and the columns, up in another order, and the
+// looped backward of the norm divides where the register one multiplies by 1 / C:
+// the same call repeats its bits, a row among more or fewer rows may not.
 #pragma clang fp contract(off)
 
 namespace {

@@ -1917,8 +1917,10 @@ void tgemm_stream(SArgs a) {
 // Bound by a step's LDS traffic and chain (barrier, fragment reads, decode,
 // barrier; about 1000 cycles for 8 waves on 128 x 128, whose products take 256):
 // without loads and decode 16384x1280x3456 still takes 68 of 107 us; whole-line A
-// loads, or A from the caches alone, change nothing, and half the barriers
-// little (36 against 44 us at best).  Measured beside it (4096x1280x3456
+// loads, or A from the caches alone, change nothing; half the barriers (steps of
+// 128, one workgroup of 128 x 160 a CU) gain where those tiles fill the CUs once
+// (4096x1280x3456 36 against 44 us) and lose elsewhere (2000x2048x2048 25 against
+// 21, 16384x1280x3456 123 against 102).  Measured beside it (4096x1280x3456
 // f32, 16384x1280x3456 bf16): 4 waves on 128 x 160 42 and 108 us, 8 on 128 x 160
 // 39 and 107, 4 on 64 x 160 42 and 148, 8 on 256 x 128 45 and 108, this 43 and
 // 107; at 2000x2048x2048, where tiles are few, 32, 27, 29, 29 and 20.

@@ -1,6 +1,6 @@
 """The product's epilogue in every kernel that its dispatch can choose: each
-tile of the tiled kernel with vector and byte loads, whole and ragged, and
-each column width of the few-row kernel, beside the shapes of
+tile of the tiled kernel with aligned and unaligned loads, whole and ragged,
+and each column width of the few-row kernel, beside the shapes of
 test_gpu_block.py.  (test_epilogue_plan.py asks the plan whether any choice is
 left out.)"""
 import pytest
