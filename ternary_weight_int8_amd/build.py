@@ -3,6 +3,8 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,26 +19,34 @@ PROBE_LIB = os.path.join(PKG, "libtgemm_roofline.so")
 ARCH = "gfx950"
 
 
-def hipcc_cmd(out: str, srcs=None) -> list[str]:
+def hipcc_cmd(out: str, *args) -> list[str]:
     return [
-        "hipcc", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+        "hipcc", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
         # no packed-fp32 instructions in device code
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-        "-I", INCLUDE, *(srcs or SRCS), "-o", out,
+        "-I", INCLUDE, *args, "-o", out,
     ]
 
 
+def _run(cmd, verbose):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("hipcc failed:\n" + r.stdout + r.stderr)
+    if verbose:
+        print(r.stderr)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile the HIP library and the probe library (always) and atomically
-    replace the old ones."""
-    for lib, srcs in ((LIB, SRCS), (PROBE_LIB, [PROBE_SRC])):
-        tmp = lib + ".tmp"
-        r = subprocess.run(hipcc_cmd(tmp, srcs), capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("hipcc failed:\n" + r.stdout + r.stderr)
-        if verbose:
-            print(r.stderr)
-        os.replace(tmp, lib)
+    """Compile the HIP library and the probe library (always; the sources side
+    by side) and atomically replace the old ones."""
+    with tempfile.TemporaryDirectory() as objs, ThreadPoolExecutor(4) as pool:
+        obj = {src: os.path.join(objs, os.path.basename(src) + ".o") for src in (*SRCS, PROBE_SRC)}
+        for done in [pool.submit(_run, hipcc_cmd(obj[src], "-c", src), verbose) for src in obj]:
+            done.result()
+        for lib, srcs in ((LIB, SRCS), (PROBE_LIB, [PROBE_SRC])):
+            tmp = lib + ".tmp"
+            _run(hipcc_cmd(tmp, "-shared", *(obj[src] for src in srcs)), verbose)
+            os.replace(tmp, lib)
     return LIB
 
 
