@@ -360,6 +360,49 @@ int ternary_epilogue_backward(const void *dY, const void *Z, int in_kind, int ac
 int ternary_epilogue_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
 
 /*
+ * Layer norm with the residual's addition, into int8 rows, as the RMS norm:
+ *     h = x + residual       rounded to the kind (h = x without a residual)
+ *     mean = sum_c h / C,  rstd = 1 / sqrt(sum_c (h - mean)^2 / C + eps)
+ *     y = ((h - mean) * rstd) * gain[c] + beta[c]
+ * and Q, scale from y.  Arguments, checks and in-place forms are those of
+ * ternary_rmsnorm_quantize, and
+ *   beta        float [C], or NULL for 0
+ *   mean, rstd  float [R] each, or both NULL (the backward pass takes them)
+ */
+int ternary_layernorm_quantize(const void *X, int in_kind, const void *residual, const float *gain, const float *beta,
+                               float eps, void *H, void *Y, float *mean, float *rstd, int8_t *Q, float *scale,
+                               int64_t R, int64_t C, hipStream_t stream);
+
+/*
+ * Its backward pass, as ternary_rmsnorm_backward.  With xhat = (h - mean) *
+ * rstd and t = dy * gain,
+ *     dX[r][c]  = rstd (t - sum_c(t) / C - xhat * sum_c(t xhat) / C) + dH[r][c]
+ *     dgain[c]  = sum_r dy * xhat,  dbeta[c] = sum_r dy
+ *   dbeta  float [C], or NULL
+ */
+int ternary_layernorm_backward(const void *dY, const void *H, int in_kind, const float *gain, const float *mean,
+                               const float *rstd, const void *dH, void *dX, float *dgain, float *dbeta, int64_t R,
+                               int64_t C, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+int ternary_layernorm_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
+
+/*
+ * Backward pass of the gated product (ternary_gemm_s8_gated), from Y's gradient
+ * and the Z = (g | u) that it saved, in one pass over both:
+ *     dg = dY * u * act'(g),  du = dY * act(g)
+ *     dZ = (dg | du)           rounded to the kind, for dW of the two matrices
+ *     dbias[c] = sum_r (dg | du)   of the unrounded values
+ *     Q, scale                 the int8 rows of (gate_scale dg | up_scale du):
+ *                              the dC of one dX call with the stored weights
+ *                              of both and a weight scale of 1
+ *   dY [R][C], Z and dZ [R][2C] of in_kind; dbias float [2C], or NULL (then no
+ *   workspace is needed); Q int8 [R][2C], scale float [R]
+ */
+int ternary_gated_backward(const void *dY, const void *Z, int in_kind, int act, float gate_scale, float up_scale,
+                           void *dZ, float *dbias, int8_t *Q, float *scale, int64_t R, int64_t C, void *workspace,
+                           int64_t workspace_bytes, hipStream_t stream);
+int ternary_gated_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
+
+/*
  * Clipping of `count` gradients by their global norm:
  *     norm = sqrt(sum over all elements of g^2)      (the sum in double)
  *     out = g * min(1, max_norm / (norm + eps))

@@ -51,6 +51,11 @@ EXPORTS = (
     "ternary_clip_grad_norm",
     "ternary_clip_grad_norm_workspace",
     "ternary_gemm_epilogue_plan",
+    "ternary_layernorm_quantize",
+    "ternary_layernorm_backward",
+    "ternary_layernorm_backward_workspace",
+    "ternary_gated_backward",
+    "ternary_gated_backward_workspace",
 )
 
 OPS = {"fwd": 0, "dx": 1, "dw": 2}
@@ -138,7 +143,12 @@ def lib():
                 ("ternary_epilogue_backward_workspace", [i64, i64, pi64]),
                 ("ternary_clip_grad_norm", [p, p, p, p, i64, f32, f32, p, p, i64, p]),
                 ("ternary_clip_grad_norm_workspace", [p, i64, pi64]),
-                ("ternary_gemm_epilogue_plan", [i64, i64, i64, i64, i32, i32, ctypes.POINTER(TgemmPlan)])):
+                ("ternary_gemm_epilogue_plan", [i64, i64, i64, i64, i32, i32, ctypes.POINTER(TgemmPlan)]),
+                ("ternary_layernorm_quantize", [p, i32, p, p, p, f32, p, p, p, p, p, p, i64, i64, p]),
+                ("ternary_layernorm_backward", [p, p, i32, p, p, p, p, p, p, p, i64, i64, p, i64, p]),
+                ("ternary_layernorm_backward_workspace", [i64, i64, pi64]),
+                ("ternary_gated_backward", [p, p, i32, i32, f32, f32, p, p, p, p, i64, i64, p, i64, p]),
+                ("ternary_gated_backward_workspace", [i64, i64, pi64])):
             f = getattr(L, name)
             f.argtypes = args
             f.restype = ctypes.c_int
@@ -735,6 +745,111 @@ def ternary_epilogue_backward(dY, Z, act="none", bias=True, dZ=None, dbias=None,
                                           0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
     return dZ, dbias, Q, scale
 
+
+def _current(device):
+    """The device the call launches on has to be its tensors'."""
+    if device.index != _torch().cuda.current_device():
+        raise ValueError(f"tensors are on {device}, and the current device is cuda:{_torch().cuda.current_device()}")
+
+
+def ternary_layernorm_quantize(X, gain, beta=None, eps=1e-5, residual=None, save=False, H=None, Y=None, mean=None,
+                               rstd=None, Q=None, scale=None, stream=None):
+    """Layer norm of h = X + residual [R][C] (float32 or bfloat16) into the int8
+    rows that the product takes: (Q int8 [R][C], scale float32 [R], H, Y, mean, rstd).
+
+    H as in ternary_rmsnorm_quantize; beta None counts as 0.  With `save`, Y
+    [R][C] in X's type holds the normed values and mean, rstd float32 [R] the
+    rows' statistics, for the backward pass; without, they are None."""
+    torch = _torch()
+    kind = _kind(X, "X")
+    _check(X, X.dtype, 2, "X")
+    (R, C), dt, dev = X.shape, X.dtype, X.device
+    _current(dev)
+    _given(gain, torch.float32, (C,), dev, "gain")
+    if beta is not None:
+        _given(beta, torch.float32, (C,), dev, "beta")
+    if residual is not None:
+        _given(residual, dt, X.shape, dev, "residual")
+        H = _like(H, X, stream, "H")
+    elif H is not None and H is not X:
+        raise ValueError("H is given without a residual: it would be X")
+    if save:
+        Y = _like(Y, X, stream, "Y")
+        mean = _made(mean, torch.float32, (R,), dev, "mean", stream)
+        rstd = _made(rstd, torch.float32, (R,), dev, "rstd", stream)
+    elif Y is not None or mean is not None or rstd is not None:
+        raise ValueError("Y, mean and rstd are outputs of save=True")
+    Q = _like(Q, X, stream, "Q", torch.int8)
+    scale = _made(scale, torch.float32, (R,), dev, "scale", stream)
+    _done("ternary_layernorm_quantize",
+          lib().ternary_layernorm_quantize(X.data_ptr(), kind, _ptr(residual), gain.data_ptr(), _ptr(beta), eps,
+                                           None if residual is None else H.data_ptr(), _ptr(Y), _ptr(mean), _ptr(rstd),
+                                           Q.data_ptr(), scale.data_ptr(), R, C, _raw_stream(stream, dev)))
+    return Q, scale, X if residual is None else H, Y, mean, rstd
+
+
+def ternary_layernorm_backward(dY, H, gain, mean, rstd, dH=None, beta=True, dX=None, dgain=None, dbeta=None,
+                               workspace=None, stream=None):
+    """(dX [R][C] in H's type, dgain float32 [C], dbeta float32 [C]; None with
+    beta=False) from the gradient dY of the normed values, the H, mean and rstd
+    that the norm kept and, with a residual stream, the gradient dH that
+    reaches H past the norm (dX may be dH)."""
+    torch = _torch()
+    kind = _kind(H, "H")
+    _check(H, H.dtype, 2, "H")
+    (R, C), dt, dev = H.shape, H.dtype, H.device
+    _current(dev)
+    _given(dY, dt, (R, C), dev, "dY")
+    _given(gain, torch.float32, (C,), dev, "gain")
+    _given(mean, torch.float32, (R,), dev, "mean")
+    _given(rstd, torch.float32, (R,), dev, "rstd")
+    if dH is not None:
+        _given(dH, dt, (R, C), dev, "dH")
+    dX = _like(dX, H, stream, "dX")
+    dgain = _like(dgain, gain, stream, "dgain")
+    if beta:
+        dbeta = _like(dbeta, gain, stream, "dbeta")
+    elif dbeta is not None:
+        raise ValueError("dbeta is an output of beta=True")
+    ws = _scratch(workspace, _queried("ternary_layernorm_backward_workspace", R, C), dev, stream)
+    _done("ternary_layernorm_backward",
+          lib().ternary_layernorm_backward(dY.data_ptr(), H.data_ptr(), kind, gain.data_ptr(), mean.data_ptr(),
+                                           rstd.data_ptr(), _ptr(dH), dX.data_ptr(), dgain.data_ptr(), _ptr(dbeta), R, C,
+                                           _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
+    return dX, dgain, dbeta
+
+
+def ternary_gated_backward(dY, Z, gate_scale, up_scale, act="silu", bias=True, dZ=None, dbias=None, Q=None, scale=None,
+                           workspace=None, stream=None):
+    """(dZ [R][2C], dbias float32 [2C], Q int8 [R][2C], scale float32 [R]) from
+    the gradient dY [R][C] of a gated product's output and the Z [R][2C] that
+    it saved, gate first: dZ for dW, its sums over the rows (None with
+    bias=False), and the int8 rows of (gate_scale dg | up_scale du) for one dX
+    call with the stored weights of both matrices and a weight scale of 1."""
+    torch = _torch()
+    kind = _kind(Z, "Z")
+    _check(Z, Z.dtype, 2, "Z")
+    (R, C2), dt, dev = Z.shape, Z.dtype, Z.device
+    _current(dev)
+    if C2 % 2:
+        raise ValueError(f"Z must have the gate's and the up projection's columns, got {C2}")
+    C = C2 // 2
+    _given(dY, dt, (R, C), dev, "dY")
+    act = _act(act)
+    dZ = _like(dZ, Z, stream, "dZ")
+    ws = None
+    if bias:
+        dbias = _made(dbias, torch.float32, (C2,), dev, "dbias", stream)
+        ws = _scratch(workspace, _queried("ternary_gated_backward_workspace", R, C), dev, stream)
+    elif dbias is not None:
+        raise ValueError("dbias is an output of bias=True")
+    Q = _like(Q, Z, stream, "Q", torch.int8)
+    scale = _made(scale, torch.float32, (R,), dev, "scale", stream)
+    _done("ternary_gated_backward",
+          lib().ternary_gated_backward(dY.data_ptr(), Z.data_ptr(), kind, act, float(gate_scale), float(up_scale),
+                                       dZ.data_ptr(), _ptr(dbias), Q.data_ptr(), scale.data_ptr(), R, C, _ptr(ws),
+                                       0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
+    return dZ, dbias, Q, scale
 
 def ternary_clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=None, stream=None):
     """(out, norm float32 [1]): the gradients scaled by min(1, max_norm / (norm

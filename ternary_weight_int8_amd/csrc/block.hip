@@ -762,12 +762,515 @@ __global__ __launch_bounds__(kNT) void col_sums(const T *__restrict__ A, const T
   P[blockIdx.y * C + c] = sum;
 }
 
+// ---------------------------------------------------------------------------
+// Layer norm.  As the RMS norm, with the mean taken off first: the mean from one
+// sum over the row, the variance from a second one over the squares of what is
+// left (from the registers: the row is still read once), so that a mean far
+// larger than the deviation loses nothing to cancellation.
+// ---------------------------------------------------------------------------
+struct LnArgs {
+  const void *X, *res;
+  const float *gain, *beta;   // beta may be null
+  void *H, *Y;
+  float *mean, *rstd, *scale;
+  int8_t *Q;
+  float eps;
+  int64_t R, C;
+};
+
+__device__ __forceinline__ float ln_y(float d, float rstd, float gain, float beta) {
+  return __builtin_fmaf(d * rstd, gain, beta);
+}
+
+template <class T>
+__global__ __launch_bounds__(kNT) void ln_rows(LnArgs a) {
+  __shared__ float part[4];
+  __shared__ uint32_t upart[4];
+  const int t = threadIdx.x;
+  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {
+    const T *x = static_cast<const T *>(a.X) + row * a.C;
+    const T *res = a.res ? static_cast<const T *>(a.res) + row * a.C : nullptr;
+    T *h = res ? static_cast<T *>(a.H) + row * a.C : nullptr;
+    float sum = 0.f;
+    for (int64_t c = t; c < a.C; c += kNT) {
+      T v = x[c];
+      if (res) {
+        v = narrow<T>(widen(v) + widen(res[c]));
+        h[c] = v;
+      }
+      sum += widen(v);
+    }
+    const float mean = __fdiv_rn(block_sum(sum, part), (float)a.C);
+    const T *src = res ? h : x;
+    float ss = 0.f;
+    for (int64_t c = t; c < a.C; c += kNT) {
+      const float d = widen(src[c]) - mean;
+      ss = __builtin_fmaf(d, d, ss);
+    }
+    const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(block_sum(ss, part), (float)a.C) + a.eps));
+    uint32_t m = 0;
+    for (int64_t c = t; c < a.C; c += kNT)
+      m = umax(m, mag(ln_y(widen(src[c]) - mean, rstd, a.gain[c], a.beta ? a.beta[c] : 0.f)));
+    const float s = __fdiv_rn(block_max(m, upart), 127.f);
+    if (t == 0) {
+      a.scale[row] = s;
+      if (a.rstd) {
+        a.mean[row] = mean;
+        a.rstd[row] = rstd;
+      }
+    }
+    int8_t *q = a.Q + row * a.C;
+    T *y = a.Y ? static_cast<T *>(a.Y) + row * a.C : nullptr;
+    for (int64_t c = t; c < a.C; c += kNT) {
+      const float v = ln_y(widen(src[c]) - mean, rstd, a.gain[c], a.beta ? a.beta[c] : 0.f);
+      if (y) y[c] = narrow<T>(v);
+      q[c] = quant1(v, s);
+    }
+  }
+}
+
+template <class T, int W, int V>
+__global__ __launch_bounds__(max_t(W, V)) void ln_reg(LnArgs a) {
+  constexpr int U = kU<T>;
+  __shared__ float part[2][16], part2[2][16];
+  __shared__ uint32_t upart[2][16];
+  const int t = W ? threadIdx.x & 63 : threadIdx.x;
+  const int grp = W ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  Units<T, W, V> un;
+  un.init((int32_t)a.C, t);
+  float gain[V][U], beta[V][U];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) beta[j][i] = 0.f;
+    if (un.on(j)) {
+      load_f<U>(a.gain + un.off[j], gain[j]);
+      if (a.beta) load_f<U>(a.beta + un.off[j], beta[j]);
+    }
+  }
+  int flip = 0;
+  const int groups = W ? (int)(blockDim.x >> 6) : 1;
+  for (int64_t row = (int64_t)blockIdx.x * groups + grp; row < a.R; row += (int64_t)gridDim.x * groups, flip ^= 1) {
+    const int64_t base = row * a.C;
+    const T *x = static_cast<const T *>(a.X) + base;
+    typename Raw<T>::V h[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) h[j] = load_raw(x + un.off[j]);
+    if (a.res) {
+      const T *res = static_cast<const T *>(a.res) + base;
+      typename Raw<T>::V r[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) r[j] = load_raw(res + un.off[j]);
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) {
+          float f[U], g[U];
+          unpack(h[j], f);
+          unpack(r[j], g);
+#pragma unroll
+          for (int i = 0; i < U; ++i) f[i] += g[i];
+          h[j] = pack(f);
+        }
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        float f[U];
+        unpack(h[j], f);
+#pragma unroll
+        for (int i = 0; i < U; ++i) sum += j == un.last && i < un.dup ? 0.f : f[i];
+      }
+    const float mean = __fdiv_rn(row_sum<W>(sum, part[flip]), (float)a.C);
+    float y[V][U], ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        unpack(h[j], y[j]);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          y[j][i] -= mean;
+          const float d = j == un.last && i < un.dup ? 0.f : y[j][i];
+          ss = __builtin_fmaf(d, d, ss);
+        }
+      }
+    ss = row_sum<W>(ss, part2[flip]);
+    const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ss, (float)a.C) + a.eps));
+    if (a.res) {
+      T *H = static_cast<T *>(a.H) + base;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) store_raw(H + un.off[j], h[j]);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          y[j][i] = ln_y(y[j][i], rstd, gain[j][i], beta[j][i]);
+          m = umax(m, mag(y[j][i]));
+        }
+      }
+    const float s = __fdiv_rn(row_max<W>(m, upart[flip]), 127.f), r = __fdiv_rn(1.f, s);
+    const bool fast = fast_scale(s);
+    if (t == 0) {
+      a.scale[row] = s;
+      if (a.rstd) {
+        a.mean[row] = mean;
+        a.rstd[row] = rstd;
+      }
+    }
+    int8_t *q = a.Q + base;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) store_q<U>(q + un.off[j], y[j], s, r, fast);
+    if (a.Y) {
+      T *Y = static_cast<T *>(a.Y) + base;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) store_raw(Y + un.off[j], pack(y[j]));
+    }
+  }
+}
+
+// Its backward pass: with xhat = (h - mean) rstd and t = dy gain,
+//     dX = rstd (t - sum t / C - xhat sum(t xhat) / C) + dH
+// Both sums of a row meet in one exchange, and the two column sums lie side by
+// side in a workgroup's row of P.
+struct LnBwdArgs {
+  const void *dY, *H;
+  const float *gain, *mean, *rstd;
+  const void *dH;
+  void *dX;
+  float *P, *P2;   // partial sums of dgain and dbeta (P2 null: none), `pitch` apart from workgroup to workgroup
+  int64_t pitch;
+  int64_t R, C;
+};
+
+template <int W>
+__device__ __forceinline__ f32x2 row_sum2(float v, float w, f32x2 *part) {
+  v = wave_sum(v);
+  w = wave_sum(w);
+  if constexpr (W == 0) {
+    const int lane = threadIdx.x & 63, l = lane & 15;
+    if (lane == 0) part[threadIdx.x >> 6] = f32x2{v, w};
+    lds_barrier();
+    const f32x2 p = l < (int)(blockDim.x >> 6) ? part[l] : f32x2{0.f, 0.f};
+    v = p[0];
+    w = p[1];
+    v += __uint_as_float(dpp<kXor1>(__float_as_uint(v)));
+    w += __uint_as_float(dpp<kXor1>(__float_as_uint(w)));
+    v += __uint_as_float(dpp<kXor2>(__float_as_uint(v)));
+    w += __uint_as_float(dpp<kXor2>(__float_as_uint(w)));
+    v += __uint_as_float(dpp<kHalfMirror>(__float_as_uint(v)));
+    w += __uint_as_float(dpp<kHalfMirror>(__float_as_uint(w)));
+    v += __uint_as_float(dpp<kMirror>(__float_as_uint(v)));
+    w += __uint_as_float(dpp<kMirror>(__float_as_uint(w)));
+  }
+  return f32x2{v, w};
+}
+
+template <class T, int W, int V>
+__global__ __launch_bounds__(max_t(W, V)) void ln_bwd_reg(LnBwdArgs a) {
+  constexpr int U = kU<T>;
+  __shared__ f32x2 part[2][16];
+  __shared__ float cols[W ? 64 * V * U : 1];
+  const int t = W ? threadIdx.x & 63 : threadIdx.x;
+  const int grp = W ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  Units<T, W, V> un;
+  un.init((int32_t)a.C, t);
+  constexpr bool kKeep = V == 1;   // as in norm_bwd_reg
+  float kept[U], acc[V][U], bacc[V][U];
+  if (kKeep && un.on(0)) load_f<U>(a.gain + un.off[0], kept);
+  auto gain_of = [&](int j, float (&g)[U]) {
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) g[i] = kept[i];
+    } else {
+      load_f<U>(a.gain + un.off[j], g);
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) acc[j][i] = bacc[j][i] = 0.f;
+  }
+  const float invC = __fdiv_rn(1.f, (float)a.C);
+  int flip = 0;
+  const int groups = W ? (int)(blockDim.x >> 6) : 1;
+  for (int64_t row = (int64_t)blockIdx.x * groups + grp; row < a.R; row += (int64_t)gridDim.x * groups, flip ^= 1) {
+    const int64_t base = row * a.C;
+    typename Raw<T>::V dy[V], h[V], dh[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        dy[j] = load_raw(static_cast<const T *>(a.dY) + base + un.off[j]);
+        h[j] = load_raw(static_cast<const T *>(a.H) + base + un.off[j]);
+      }
+    if (a.dH) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) dh[j] = load_raw(static_cast<const T *>(a.dH) + base + un.off[j]);
+    }
+    const float rstd = a.rstd[row], mean = a.mean[row];
+    float st = 0.f, sx = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        float d[U], f[U], gain[U], pt = 0.f, px = 0.f;
+        gain_of(j, gain);
+        unpack(dy[j], d);
+        unpack(h[j], f);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const float g = d[i] * ((f[i] - mean) * rstd);
+          acc[j][i] += g;
+          bacc[j][i] += d[i];
+          // left out by not adding it: a zero factor would make an infinity a NaN
+          const bool twice = j == un.last && i < un.dup;
+          pt = twice ? pt : __builtin_fmaf(d[i], gain[i], pt);
+          px = twice ? px : __builtin_fmaf(g, gain[i], px);
+        }
+        st += pt;
+        sx += px;
+      }
+    if (W == 0 && a.dH) {
+      // as in norm_bwd_reg: dX may be dH itself
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) asm volatile("" : "+v"(dh[j]));
+    }
+    const f32x2 sums = row_sum2<W>(st, sx, part[flip]);
+    const float mt = sums[0] * invC, mx = sums[1] * invC;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        float d[U], f[U], gain[U];
+        gain_of(j, gain);
+        unpack(dy[j], d);
+        unpack(h[j], f);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          d[i] = rstd * __builtin_fmaf(-((f[i] - mean) * rstd), mx, __builtin_fmaf(d[i], gain[i], -mt));
+        if (a.dH) {
+          unpack(dh[j], f);
+#pragma unroll
+          for (int i = 0; i < U; ++i) d[i] += f[i];
+        }
+        store_raw(static_cast<T *>(a.dX) + base + un.off[j], pack(d));
+      }
+  }
+  write_cols<T, W, V>(acc, un, grp, cols, a.P + (int64_t)blockIdx.x * a.pitch);
+  if (a.P2) write_cols<T, W, V>(bacc, un, grp, cols, a.P2 + (int64_t)blockIdx.x * a.pitch);
+}
+
+template <class T>
+__global__ __launch_bounds__(kNT) void ln_bwd_rows(LnBwdArgs a) {
+  __shared__ float part[4];
+  const int t = threadIdx.x;
+  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {
+    const T *dy = static_cast<const T *>(a.dY) + row * a.C;
+    const T *h = static_cast<const T *>(a.H) + row * a.C;
+    const T *dh = a.dH ? static_cast<const T *>(a.dH) + row * a.C : nullptr;
+    T *dx = static_cast<T *>(a.dX) + row * a.C;
+    const float rstd = a.rstd[row], mean = a.mean[row];
+    float st = 0.f, sx = 0.f;
+    for (int64_t c = t; c < a.C; c += kNT) {
+      const float v = widen(dy[c]) * a.gain[c];
+      st += v;
+      sx = __builtin_fmaf(v, (widen(h[c]) - mean) * rstd, sx);
+    }
+    const float mt = __fdiv_rn(block_sum(st, part), (float)a.C), mx = __fdiv_rn(block_sum(sx, part), (float)a.C);
+    for (int64_t c = t; c < a.C; c += kNT) {
+      float v = rstd * __builtin_fmaf(-((widen(h[c]) - mean) * rstd), mx, __builtin_fmaf(widen(dy[c]), a.gain[c], -mt));
+      if (dh) v += widen(dh[c]);
+      dx[c] = narrow<T>(v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward of the gated product: row r of Z holds the gate's values z and, C
+// further, the up projection's u.
+//     dz = dy u act'(z),  du = dy act(z)
+// dZ, the int8 rows and the column sums have the same two halves; the int8 rows
+// are of (kz dz | ku du), k the scales of the two weight matrices, so that one
+// product with both matrices' codes adds the two parts of dX up.
+// ---------------------------------------------------------------------------
+struct GatedBwdArgs {
+  const void *dY, *Z;
+  void *dZ;
+  int8_t *Q;
+  float *scale;
+  float *P;       // [gridDim.x][2 C], or null
+  float kz, ku;
+  int64_t R, C;
+  int32_t act;
+};
+
+// (dz, du) of z sigmoid(u(z)), in the terms of back_sigm.  Below -lim act(z) is
+// taken there: it is less than 1e-35 from 0, its limit, either way.
+__device__ __forceinline__ f32x2 gated_sigm(float dy, float z, float u, const Sigm &k) {
+  const float c = fminf(fmaxf(z, -k.lim), k.lim), c2 = c * c;
+  const float e = __builtin_amdgcn_exp2f(c * __builtin_fmaf(k.k1, c2, k.k0));
+  const float p = __builtin_amdgcn_rcpf(1.f + e);
+  const float w = c * __builtin_fmaf(k.d1, c2, k.d0) * (e * p);
+  const float dz = (dy * u) * __builtin_fmaf(w, p, p), du = dy * (fmaxf(z, -k.lim) * p);
+  return z == z ? f32x2{dz, du} : f32x2{z, z};   // the clamps drop a NaN
+}
+__device__ __forceinline__ f32x2 gated_poly(float dy, float z, float u, int act) {
+  const float t = dy * u;
+  if (act == TGEMM_ACT_NONE) return f32x2{t, dy * z};
+  const float p = z < 0.f ? 0.f : z;   // a NaN stays one
+  return act == TGEMM_ACT_RELU ? f32x2{back_relu(t, z), dy * p} : f32x2{back_relu2(t, z), (dy * p) * p};
+}
+__device__ __forceinline__ f32x2 gated_back(float dy, float z, float u, int act) {
+  return is_sigm(act) ? gated_sigm(dy, z, u, sigm_of(act)) : gated_poly(dy, z, u, act);
+}
+
+template <class T, int W, int V, int S>
+__global__ __launch_bounds__(max_t(W, V)) void gated_bwd_reg(GatedBwdArgs a) {
+  constexpr int U = kU<T>;
+  __shared__ uint32_t upart[2][16];
+  __shared__ float cols[W ? 64 * V * U : 1];
+  const int t = W ? threadIdx.x & 63 : threadIdx.x;
+  const int grp = W ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  Units<T, W, V> un;
+  un.init((int32_t)a.C, t);
+  float zacc[V][U], uacc[V][U];
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+#pragma unroll
+    for (int i = 0; i < U; ++i) zacc[j][i] = uacc[j][i] = 0.f;
+  const Sigm sg = sigm_of(a.act);
+  int flip = 0;
+  const int groups = W ? (int)(blockDim.x >> 6) : 1;
+  for (int64_t row = (int64_t)blockIdx.x * groups + grp; row < a.R; row += (int64_t)gridDim.x * groups, flip ^= 1) {
+    const int64_t base = row * a.C, zbase = 2 * base;
+    typename Raw<T>::V dy[V], z[V], u[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        dy[j] = load_raw(static_cast<const T *>(a.dY) + base + un.off[j]);
+        z[j] = load_raw(static_cast<const T *>(a.Z) + zbase + un.off[j]);
+        u[j] = load_raw(static_cast<const T *>(a.Z) + zbase + a.C + un.off[j]);
+      }
+    float dz[V][U], du[V][U];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        float d[U];
+        unpack(dy[j], d);
+        unpack(z[j], dz[j]);
+        unpack(u[j], du[j]);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          f32x2 v;
+          if constexpr (S)
+            v = gated_sigm(d[i], dz[j][i], du[j][i], sg);
+          else
+            v = gated_poly(d[i], dz[j][i], du[j][i], a.act);
+          dz[j][i] = v[0];
+          du[j][i] = v[1];
+          zacc[j][i] += v[0];
+          uacc[j][i] += v[1];
+          m = umax(m, umax(mag(v[0] * a.kz), mag(v[1] * a.ku)));
+        }
+      }
+    const float s = __fdiv_rn(row_max<W>(m, upart[flip]), 127.f), r = __fdiv_rn(1.f, s);
+    const bool fast = fast_scale(s);
+    if (t == 0) a.scale[row] = s;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (un.on(j)) {
+        store_raw(static_cast<T *>(a.dZ) + zbase + un.off[j], pack(dz[j]));
+        store_raw(static_cast<T *>(a.dZ) + zbase + a.C + un.off[j], pack(du[j]));
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          dz[j][i] *= a.kz;
+          du[j][i] *= a.ku;
+        }
+        store_q<U>(a.Q + zbase + un.off[j], dz[j], s, r, fast);
+        store_q<U>(a.Q + zbase + a.C + un.off[j], du[j], s, r, fast);
+      }
+  }
+  if (a.P) {
+    float *P = a.P + (int64_t)blockIdx.x * 2 * a.C;
+    write_cols<T, W, V>(zacc, un, grp, cols, P);
+    write_cols<T, W, V>(uacc, un, grp, cols, P + a.C);
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(kNT) void gated_bwd_rows(GatedBwdArgs a) {
+  __shared__ uint32_t upart[4];
+  const int t = threadIdx.x;
+  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {
+    const T *dy = static_cast<const T *>(a.dY) + row * a.C;
+    const T *z = static_cast<const T *>(a.Z) + 2 * row * a.C, *u = z + a.C;
+    T *dz = static_cast<T *>(a.dZ) + 2 * row * a.C;
+    int8_t *q = a.Q + 2 * row * a.C;
+    uint32_t m = 0;
+    for (int64_t c = t; c < a.C; c += kNT) {
+      const f32x2 v = gated_back(widen(dy[c]), widen(z[c]), widen(u[c]), a.act);
+      dz[c] = narrow<T>(v[0]);
+      dz[a.C + c] = narrow<T>(v[1]);
+      m = umax(m, umax(mag(v[0] * a.kz), mag(v[1] * a.ku)));
+    }
+    const float s = __fdiv_rn(block_max(m, upart), 127.f);
+    if (t == 0) a.scale[row] = s;
+    for (int64_t c = t; c < a.C; c += kNT) {
+      const f32x2 v = gated_back(widen(dy[c]), widen(z[c]), widen(u[c]), a.act);
+      q[c] = quant1(v[0] * a.kz, s);
+      q[a.C + c] = quant1(v[1] * a.ku, s);
+    }
+  }
+}
+
+// Partial column sums of the two looped backward passes, as col_sums: two
+// sums a column, C apart in a row of P
+struct Cols2Args {
+  const void *A, *B;           // dY, and H or Z
+  const float *mean, *rstd;    // layer norm
+  float *P;                    // [strips][pitch]
+  int64_t pitch;               // 2 C, or C for the first sums alone
+  int64_t R, C, strip;
+  int32_t act;                 // gated
+};
+template <class T, bool NORM>
+__global__ __launch_bounds__(kNT) void col_sums2(Cols2Args k) {
+  const int64_t c = (int64_t)blockIdx.x * kNT + threadIdx.x;
+  if (c >= k.C) return;
+  const T *A = static_cast<const T *>(k.A), *B = static_cast<const T *>(k.B);
+  const int64_t r0 = (int64_t)blockIdx.y * k.strip, r1 = r0 + k.strip < k.R ? r0 + k.strip : k.R;
+  float s0 = 0.f, s1 = 0.f;
+  for (int64_t r = r0; r < r1; ++r) {
+    const float a = widen(A[r * k.C + c]);
+    if constexpr (NORM) {
+      s0 = __builtin_fmaf(a, (widen(B[r * k.C + c]) - k.mean[r]) * k.rstd[r], s0);
+      s1 += a;
+    } else {
+      const f32x2 v = gated_back(a, widen(B[2 * r * k.C + c]), widen(B[(2 * r + 1) * k.C + c]), k.act);
+      s0 += v[0];
+      s1 += v[1];
+    }
+  }
+  float *P = k.P + blockIdx.y * k.pitch;
+  P[c] = s0;
+  if (k.pitch > k.C) P[k.C + c] = s1;
+}
+
 // the rows of P added up: a workgroup takes 32 columns, its 32 groups of 32
 // threads each every 32nd row, eight loads at a time, and the groups' sums
 // meet in LDS in order
 constexpr int kFinCols = 32, kFinGroups = 32, kFinT = kFinCols * kFinGroups;
-__global__ __launch_bounds__(kFinT) void col_finish(const float *__restrict__ P, float *__restrict__ out, int64_t rows,
-                                                    int64_t C) {
+// (columns from `split` on go to out2: the sums of two operands side by side)
+__global__ __launch_bounds__(kFinT) void col_finish(const float *__restrict__ P, float *__restrict__ out,
+                                                    float *__restrict__ out2, int64_t split, int64_t rows, int64_t C) {
   __shared__ float part[kFinGroups][kFinCols + 1];
   const int c = threadIdx.x % kFinCols, g = threadIdx.x / kFinCols;
   const int64_t col = (int64_t)blockIdx.x * kFinCols + c;
@@ -785,7 +1288,10 @@ __global__ __launch_bounds__(kFinT) void col_finish(const float *__restrict__ P,
   if (g == 0 && col < C) {
 #pragma unroll
     for (int i = 1; i < kFinGroups; ++i) sum += part[i][c];
-    out[col] = sum;
+    if (col < split)
+      out[col] = sum;
+    else
+      out2[col - split] = sum;
   }
 }
 
@@ -1016,7 +1522,13 @@ int done() { return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP; 
 
 
 void launch_finish(const float *P, float *out, int64_t rows, int64_t C, hipStream_t stream) {
-  hipLaunchKernelGGL(col_finish, dim3((unsigned)ceil_div(C, kFinCols)), dim3(kFinT), 0, stream, P, out, rows, C);
+  hipLaunchKernelGGL(col_finish, dim3((unsigned)ceil_div(C, kFinCols)), dim3(kFinT), 0, stream, P, out, nullptr, C,
+                     rows, C);
+}
+// rows of two sums side by side, C columns each (out2 null: of the first alone)
+void launch_finish2(const float *P, float *out, float *out2, int64_t rows, int64_t C, hipStream_t stream) {
+  const int64_t n = out2 ? 2 * C : C;
+  hipLaunchKernelGGL(col_finish, dim3((unsigned)ceil_div(n, kFinCols)), dim3(kFinT), 0, stream, P, out, out2, C, rows, n);
 }
 
 // W and V of the register kernels, for rows of U to 16384 elements: a wave a
@@ -1097,6 +1609,10 @@ ROW_KERNEL(NormReg, false, NormArgs, norm_reg<T, W, V>)
 ROW_KERNEL(NormBwdReg, true, NormBwdArgs, norm_bwd_reg<T, W, V>)
 ROW_KERNEL(EpiBwdPoly, true, EpiBwdArgs, epi_bwd_reg<T, W, V, 0>)
 ROW_KERNEL(EpiBwdSigm, true, EpiBwdArgs, epi_bwd_reg<T, W, V, 1>)
+ROW_KERNEL(LnReg, false, LnArgs, ln_reg<T, W, V>)
+ROW_KERNEL(LnBwdReg, true, LnBwdArgs, ln_bwd_reg<T, W, V>)
+ROW_KERNEL(GatedBwdPoly, true, GatedBwdArgs, gated_bwd_reg<T, W, V, 0>)
+ROW_KERNEL(GatedBwdSigm, true, GatedBwdArgs, gated_bwd_reg<T, W, V, 1>)
 #undef ROW_KERNEL
 template <class Kernel>
 void row_launch(int kind, const RowPlan &p, const typename Kernel::Args &a, hipStream_t stream) {
@@ -1129,6 +1645,22 @@ void launch_cols(const T *A, const T *B, const float *rstd, int act, float *P, f
   hipLaunchKernelGGL((col_sums<T, NORM>), dim3(gx, (unsigned)strips), dim3(kNT), 0, stream, A, B, rstd, act, P, R, C,
                      strip);
   launch_finish(P, out, strips, C, stream);
+}
+
+template <class T, bool NORM>
+void launch_cols2(Cols2Args k, float *out, float *out2, hipStream_t stream) {
+  k.pitch = out2 ? 2 * k.C : k.C;
+  k.strip = ceil_div(k.R, strips_of(k.R));
+  const int64_t strips = ceil_div(k.R, k.strip);
+  hipLaunchKernelGGL((col_sums2<T, NORM>), dim3((unsigned)ceil_div(k.C, kNT), (unsigned)strips), dim3(kNT), 0, stream, k);
+  launch_finish2(k.P, out, out2, strips, k.C, stream);
+}
+template <bool NORM>
+void launch_cols2(int kind, const Cols2Args &k, float *out, float *out2, hipStream_t stream) {
+  if (kind == TGEMM_IN_F32)
+    launch_cols2<float, NORM>(k, out, out2, stream);
+  else
+    launch_cols2<uint16_t, NORM>(k, out, out2, stream);
 }
 
 }  // namespace
@@ -1246,6 +1778,114 @@ int ternary_epilogue_backward(const void *dY, const void *Z, int in_kind, int ac
       launch_cols<uint16_t, false>(static_cast<const uint16_t *>(dY), static_cast<const uint16_t *>(Z), nullptr, act,
                                    P, dbias, R, C, stream);
   }
+  return done();
+}
+
+int ternary_layernorm_quantize(const void *X, int in_kind, const void *residual, const float *gain, const float *beta,
+                               float eps, void *H, void *Y, float *mean, float *rstd, int8_t *Q, float *scale, int64_t R,
+                               int64_t C, hipStream_t stream) {
+  if (!X || !gain || !Q || !scale || (residual && !H) || !mean != !rstd) return TGEMM_ERR_NULL;
+  const int st = check_rc(in_kind, R, C);
+  if (st != TGEMM_OK) return st;
+  if (!(eps >= 0.f && eps < __builtin_inff())) return TGEMM_ERR_VALUE;
+  if (!residual) H = nullptr;
+  const int64_t n = R * C, xb = n * (in_kind == TGEMM_IN_F32 ? 4 : 2);
+  const Buf outs[] = {{H, xb}, {Y, xb}, {mean, 4 * R}, {rstd, 4 * R}, {Q, n}, {scale, 4 * R}};
+  const Buf ins[] = {{X, xb}, {residual, xb}, {gain, 4 * C}, {beta, 4 * C}};
+  const void *const same[6][2] = {{X, residual}};
+  if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
+  const LnArgs a = {X, residual, gain, beta, H, Y, mean, rstd, scale, Q, eps, R, C};
+  const RowPlan p = row_plan(R, C, in_kind, false);
+  if (p.v) {
+    row_launch<LnReg>(in_kind, p, a, stream);
+    return done();
+  }
+  const dim3 g((unsigned)(R < kMaxRowGrid ? R : kMaxRowGrid));
+  if (in_kind == TGEMM_IN_F32)
+    hipLaunchKernelGGL(ln_rows<float>, g, dim3(kNT), 0, stream, a);
+  else
+    hipLaunchKernelGGL(ln_rows<uint16_t>, g, dim3(kNT), 0, stream, a);
+  return done();
+}
+
+int ternary_layernorm_backward_workspace(int64_t R, int64_t C, int64_t *bytes) {
+  if (!bytes) return TGEMM_ERR_NULL;
+  const int st = check_rc(TGEMM_IN_F32, R, C);
+  if (st != TGEMM_OK) return st;
+  *bytes = 2 * col_ws_bytes(R, C);
+  return TGEMM_OK;
+}
+
+int ternary_layernorm_backward(const void *dY, const void *H, int in_kind, const float *gain, const float *mean,
+                               const float *rstd, const void *dH, void *dX, float *dgain, float *dbeta, int64_t R,
+                               int64_t C, void *workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (!dY || !H || !gain || !mean || !rstd || !dX || !dgain) return TGEMM_ERR_NULL;
+  const int st = check_rc(in_kind, R, C);
+  if (st != TGEMM_OK) return st;
+  if (!workspace_ok(workspace, workspace_bytes, 2 * col_ws_bytes(R, C))) return TGEMM_ERR_WORKSPACE;
+  const int64_t xb = R * C * (in_kind == TGEMM_IN_F32 ? 4 : 2);
+  const Buf outs[] = {{dX, xb}, {dgain, 4 * C}, {dbeta, 4 * C}, {workspace, workspace_bytes > 0 ? workspace_bytes : 0}};
+  const Buf ins[] = {{dY, xb}, {H, xb}, {gain, 4 * C}, {mean, 4 * R}, {rstd, 4 * R}, {dH, xb}};
+  const void *const same[4][2] = {{dH, dH}};
+  if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
+  float *P = static_cast<float *>(workspace);
+  LnBwdArgs a = {dY, H, gain, mean, rstd, dH, dX, P, dbeta ? P + C : nullptr, dbeta ? 2 * C : C, R, C};
+  const RowPlan p = row_plan(R, C, in_kind, true);
+  if (p.v) {
+    if (p.grid == 1) {
+      a.P = dgain;
+      a.P2 = dbeta;
+    }
+    row_launch<LnBwdReg>(in_kind, p, a, stream);
+    if (p.grid > 1) launch_finish2(P, dgain, dbeta, p.grid, C, stream);
+    return done();
+  }
+  const dim3 g((unsigned)(R < kMaxRowGrid ? R : kMaxRowGrid));
+  if (in_kind == TGEMM_IN_F32)
+    hipLaunchKernelGGL(ln_bwd_rows<float>, g, dim3(kNT), 0, stream, a);
+  else
+    hipLaunchKernelGGL(ln_bwd_rows<uint16_t>, g, dim3(kNT), 0, stream, a);
+  launch_cols2<true>(in_kind, {dY, H, mean, rstd, P, 0, R, C, 0, 0}, dgain, dbeta, stream);
+  return done();
+}
+
+int ternary_gated_backward_workspace(int64_t R, int64_t C, int64_t *bytes) {
+  return ternary_layernorm_backward_workspace(R, C, bytes);
+}
+
+int ternary_gated_backward(const void *dY, const void *Z, int in_kind, int act, float gate_scale, float up_scale,
+                           void *dZ, float *dbias, int8_t *Q, float *scale, int64_t R, int64_t C, void *workspace,
+                           int64_t workspace_bytes, hipStream_t stream) {
+  if (!dY || !Z || !dZ || !Q || !scale) return TGEMM_ERR_NULL;
+  const int st = check_rc(in_kind, R, C);
+  if (st != TGEMM_OK) return st;
+  if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_VALUE;
+  const int64_t wb = dbias ? 2 * col_ws_bytes(R, C) : 0;
+  if (!workspace_ok(workspace, workspace_bytes, wb)) return TGEMM_ERR_WORKSPACE;
+  const int64_t n = R * C, xb = n * (in_kind == TGEMM_IN_F32 ? 4 : 2);
+  const Buf outs[] = {{dZ, 2 * xb}, {dbias, 8 * C}, {Q, 2 * n}, {scale, 4 * R},
+                      {workspace, workspace_bytes > 0 ? workspace_bytes : 0}};
+  const Buf ins[] = {{dY, xb}, {Z, 2 * xb}};
+  const void *const same[5][2] = {};
+  if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
+  float *P = static_cast<float *>(workspace);
+  GatedBwdArgs a = {dY, Z, dZ, Q, scale, dbias ? P : nullptr, gate_scale, up_scale, R, C, act};
+  const RowPlan p = row_plan(R, C, in_kind, true);
+  if (p.v) {
+    if (p.grid == 1) a.P = dbias;
+    if (is_sigm(act))
+      row_launch<GatedBwdSigm>(in_kind, p, a, stream);
+    else
+      row_launch<GatedBwdPoly>(in_kind, p, a, stream);
+    if (dbias && p.grid > 1) launch_finish(P, dbias, p.grid, 2 * C, stream);
+    return done();
+  }
+  const dim3 g((unsigned)(R < kMaxRowGrid ? R : kMaxRowGrid));
+  if (in_kind == TGEMM_IN_F32)
+    hipLaunchKernelGGL(gated_bwd_rows<float>, g, dim3(kNT), 0, stream, a);
+  else
+    hipLaunchKernelGGL(gated_bwd_rows<uint16_t>, g, dim3(kNT), 0, stream, a);
+  if (dbias) launch_cols2<false>(in_kind, {dY, Z, nullptr, nullptr, P, 0, R, C, 0, act}, dbias, dbias + C, stream);
   return done();
 }
 
