@@ -386,6 +386,55 @@ int ternary_layernorm_backward(const void *dY, const void *H, int in_kind, const
 int ternary_layernorm_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
 
 /*
+ * Product of int8 rows with int8 weights, a scale for each row (token) and one
+ * for each column (channel), with the epilogue of ternary_gemm_s8_epilogue:
+ *     z = (float(acc) * a_row_scale[m]) * w_col_scale[n] + bias[n]
+ *     Y[m][n] = act(z) + residual[m][n]
+ * in float32, acc[m][n] = sum_k A[m][k] * W[n][k] exact, each stored matrix
+ * rounded once.  For layers that stay at 8 bits beside ternary ones (the first,
+ * the head); ternary_quantize_rows makes A, W and both scales.
+ *   A            int8 [M][K]
+ *   W            int8 [N][K]  (row n: the weights of output column n)
+ *   a_row_scale  float [M]
+ *   w_col_scale  float [N], or NULL for 1
+ *   bias, act, residual, Y, Z  as in ternary_gemm_s8_epilogue
+ * Any K up to TGEMM_INT8_MAX_CONTRACTION (TGEMM_ERR_BOUND).  Its gradients: dX is
+ * this call on dZ's int8 rows and the transposed weights, quantized row by row
+ * like the weights; dW is ternary_gemm_s8_dw_scaled on both operands' columns.
+ * Workspace: where K is not a multiple of 16 or an operand's base not 16-byte
+ * aligned, more than 64 rows need it (the operand is copied into aligned rows).
+ * The query takes the smallest alignment of A and W, in bytes.
+ */
+int ternary_gemm_s8s8_epilogue(const int8_t *A, const int8_t *W, const float *a_row_scale, const float *w_col_scale,
+                               const float *bias, int act, const void *residual, void *Y, void *Z, int out_kind,
+                               int64_t M, int64_t N, int64_t K, void *workspace, int64_t workspace_bytes,
+                               hipStream_t stream);
+int ternary_gemm_s8s8_workspace(int64_t M, int64_t N, int64_t K, int64_t align, int64_t *bytes);
+
+/*
+ * Gated product: the two projections of a gated feed-forward layer, the
+ * activation and the product in one pass,
+ *     g = (float(acc_g) * a_row_scale[m]) * gate_scale + bias[n]
+ *     u = (float(acc_u) * a_row_scale[m]) * up_scale + bias[N + n]
+ *     Y[m][n] = act(g) * u
+ * in float32, acc_g and acc_u the exact ternary products with the gate's and the
+ * up projection's weights, each stored matrix rounded once.
+ *   A        int8 [M][K]
+ *   Wpacked  uint8 [2N][K/4], stored ternary weights: the gate's N rows, then the
+ *            up projection's (one matrix for the dX and dW calls)
+ *   bias     float [2N], or NULL
+ *   Y        [M][N] of out_kind
+ *   Z        [M][2N] of out_kind, (g | u) for ternary_gated_backward, or NULL
+ * Workspace: more than 64 rows need one (the weights' codes are decoded into it,
+ * 2 N K bytes), and so do fewer where K is not a multiple of 64 or A or Wpacked
+ * not 16-byte aligned.  The query takes their smallest alignment, in bytes.
+ */
+int ternary_gemm_s8_gated(const int8_t *A, const uint8_t *Wpacked, const float *a_row_scale, float gate_scale,
+                          float up_scale, const float *bias, int act, void *Y, void *Z, int out_kind, int64_t M,
+                          int64_t N, int64_t K, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+int ternary_gemm_s8_gated_workspace(int64_t M, int64_t N, int64_t K, int64_t align, int64_t *bytes);
+
+/*
  * Backward pass of the gated product (ternary_gemm_s8_gated), from Y's gradient
  * and the Z = (g | u) that it saved, in one pass over both:
  *     dg = dY * u * act'(g),  du = dY * act(g)

@@ -56,6 +56,10 @@ EXPORTS = (
     "ternary_layernorm_backward_workspace",
     "ternary_gated_backward",
     "ternary_gated_backward_workspace",
+    "ternary_gemm_s8s8_epilogue",
+    "ternary_gemm_s8s8_workspace",
+    "ternary_gemm_s8_gated",
+    "ternary_gemm_s8_gated_workspace",
 )
 
 OPS = {"fwd": 0, "dx": 1, "dw": 2}
@@ -148,7 +152,11 @@ def lib():
                 ("ternary_layernorm_backward", [p, p, i32, p, p, p, p, p, p, p, i64, i64, p, i64, p]),
                 ("ternary_layernorm_backward_workspace", [i64, i64, pi64]),
                 ("ternary_gated_backward", [p, p, i32, i32, f32, f32, p, p, p, p, i64, i64, p, i64, p]),
-                ("ternary_gated_backward_workspace", [i64, i64, pi64])):
+                ("ternary_gated_backward_workspace", [i64, i64, pi64]),
+                ("ternary_gemm_s8s8_epilogue", [p, p, p, p, p, i32, p, p, p, i32, i64, i64, i64, p, i64, p]),
+                ("ternary_gemm_s8s8_workspace", [i64, i64, i64, i64, pi64]),
+                ("ternary_gemm_s8_gated", [p, p, p, f32, f32, p, i32, p, p, i32, i64, i64, i64, p, i64, p]),
+                ("ternary_gemm_s8_gated_workspace", [i64, i64, i64, i64, pi64])):
             f = getattr(L, name)
             f.argtypes = args
             f.restype = ctypes.c_int
@@ -818,6 +826,78 @@ def ternary_layernorm_backward(dY, H, gain, mean, rstd, dH=None, beta=True, dX=N
                                            _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
     return dX, dgain, dbeta
 
+
+def ternary_gemm_s8s8_epilogue(A, W, a_row_scale, w_col_scale=None, bias=None, act="none", residual=None, out_dtype=None,
+                               save=False, Y=None, Z=None, workspace=None, stream=None):
+    """(Y, Z): Y [M][N] = act(z) + residual with z = (float(A x W^T) *
+    a_row_scale[m]) * w_col_scale[n] + bias[n], of int8 rows A [M][K] and int8
+    weights W [N][K]; w_col_scale None counts as 1.  The other arguments are
+    ternary_gemm_s8_epilogue's."""
+    torch = _torch()
+    out_dtype = out_dtype or torch.bfloat16
+    _check(A, torch.int8, 2, "A")
+    _check(W, torch.int8, 2, "W")
+    (M, K), dev = A.shape, A.device
+    N = W.shape[0]
+    if W.shape[1] != K or W.device != dev:
+        raise ValueError(f"W must be [N][K] = [{N}][{K}] on {dev}, got {tuple(W.shape)} on {W.device}")
+    _current(dev)
+    _given(a_row_scale, torch.float32, (M,), dev, "a_row_scale")
+    if w_col_scale is not None:
+        _given(w_col_scale, torch.float32, (N,), dev, "w_col_scale")
+    if bias is not None:
+        _given(bias, torch.float32, (N,), dev, "bias")
+    kind, act = _out_kind(out_dtype), _act(act)
+    if residual is not None:
+        _given(residual, out_dtype, (M, N), dev, "residual")
+    if Z is not None and not save:
+        raise ValueError("Z is an output of save=True")
+    Y = _made(Y, out_dtype, (M, N), dev, "Y", stream)
+    if save:
+        Z = _made(Z, out_dtype, (M, N), dev, "Z", stream)
+    a, w = A.data_ptr(), W.data_ptr()
+    ws = _scratch(workspace, _queried("ternary_gemm_s8s8_workspace", M, N, K, min(_lowbit(a), _lowbit(w))), dev, stream)
+    _done("ternary_gemm_s8s8_epilogue",
+          lib().ternary_gemm_s8s8_epilogue(a, w, a_row_scale.data_ptr(), _ptr(w_col_scale), _ptr(bias), act,
+                                           _ptr(residual), Y.data_ptr(), _ptr(Z), kind, M, N, K, _ptr(ws),
+                                           0 if ws is None else ws.numel(), _raw_stream(stream, dev)))
+    return Y, Z
+
+
+def ternary_gemm_s8_gated(A, Wpacked, a_row_scale, gate_scale, up_scale, bias=None, act="silu", out_dtype=None,
+                          save=False, Y=None, Z=None, workspace=None, stream=None):
+    """(Y, Z): Y [M][N] = act(g) * u, the gated layer of int8 rows A [M][K] and
+    stored ternary weights Wpacked [2N][K/4], the gate's rows before the up
+    projection's: g = (float(A x Wg) * a_row_scale[m]) * gate_scale + bias[n],
+    u likewise with up_scale and bias[N + n].  With `save`, Z [M][2N] holds
+    (g | u) for ternary_gated_backward; without, it is None."""
+    torch = _torch()
+    out_dtype = out_dtype or torch.bfloat16
+    _check(A, torch.int8, 2, "A")
+    _check(Wpacked, torch.uint8, 2, "Wpacked")
+    (M, K), dev = A.shape, A.device
+    N2, kb = Wpacked.shape
+    if kb * 4 != K or N2 % 2 or Wpacked.device != dev:
+        raise ValueError(f"Wpacked must be [2N][K/4] with K/4 = {K // 4} on {dev}, got {tuple(Wpacked.shape)} on "
+                         f"{Wpacked.device}")
+    _current(dev)
+    N = N2 // 2
+    _given(a_row_scale, torch.float32, (M,), dev, "a_row_scale")
+    if bias is not None:
+        _given(bias, torch.float32, (N2,), dev, "bias")
+    kind, act = _out_kind(out_dtype), _act(act)
+    if Z is not None and not save:
+        raise ValueError("Z is an output of save=True")
+    Y = _made(Y, out_dtype, (M, N), dev, "Y", stream)
+    if save:
+        Z = _made(Z, out_dtype, (M, N2), dev, "Z", stream)
+    a, w = A.data_ptr(), Wpacked.data_ptr()
+    ws = _scratch(workspace, _queried("ternary_gemm_s8_gated_workspace", M, N, K, min(_lowbit(a), _lowbit(w))), dev, stream)
+    _done("ternary_gemm_s8_gated",
+          lib().ternary_gemm_s8_gated(a, w, a_row_scale.data_ptr(), float(gate_scale), float(up_scale), _ptr(bias), act,
+                                      Y.data_ptr(), _ptr(Z), kind, M, N, K, _ptr(ws), 0 if ws is None else ws.numel(),
+                                      _raw_stream(stream, dev)))
+    return Y, Z
 
 def ternary_gated_backward(dY, Z, gate_scale, up_scale, act="silu", bias=True, dZ=None, dbias=None, Q=None, scale=None,
                            workspace=None, stream=None):

@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <vector>
 
+#include "checks.h"
 #include "ternary_gemm.h"
 
 // Sums and products are fused only where fma is written, so that a kernel
@@ -34,13 +35,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr int kNT = 256;   // threads per workgroup
 constexpr int64_t kCUs = 256;                        // compute units of an MI355X
 constexpr int64_t kNormWaves = 32, kBwdWaves = 16;   // waves a CU of the row kernels' grids, at most
-
-bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a && b && an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
-}
-bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -1455,26 +1449,6 @@ int check_rc(int kind, int64_t R, int64_t C) {
   return TGEMM_OK;
 }
 
-struct Buf {
-  const void *p;
-  int64_t bytes;
-};
-// whether outs[i] overlaps an input (equal pointers allowed where `same` names
-// that input for it) or a later output; NULL buffers overlap nothing
-template <int NO, int NI>
-bool alias(const Buf (&outs)[NO], const Buf (&ins)[NI], const void *const (&same)[NO][2]) {
-  for (int i = 0; i < NO; ++i) {
-    for (int j = 0; j < NI; ++j)
-      if (overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes) &&
-          !(outs[i].p == ins[j].p && outs[i].bytes == ins[j].bytes &&
-            (ins[j].p == same[i][0] || ins[j].p == same[i][1])))
-        return true;
-    for (int j = i + 1; j < NO; ++j)
-      if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
-  }
-  return false;
-}
-
 // whether an output of the lists overlaps another output or another gradient:
 // the ranges sorted by address, each compared with the furthest end of the
 // outputs (for a gradient) or of all ranges (for an output) before it
@@ -1633,10 +1607,6 @@ int64_t col_ws_bytes(int64_t R, int64_t C) {
   }
   return 4 * rows * C;
 }
-bool workspace_ok(const void *ws, int64_t bytes, int64_t need) {
-  return need == 0 || (ws && bytes >= need && aligned(ws, 16));
-}
-
 template <class T, bool NORM>
 void launch_cols(const T *A, const T *B, const float *rstd, int act, float *P, float *out, int64_t R, int64_t C,
                  hipStream_t stream) {

@@ -1,0 +1,629 @@
+// int8.hip -- gfx950 kernels of two products, part of libternary_gemm.so (ABI and
+// formulas in include/ternary_gemm.h):
+//   ternary_gemm_s8s8_epilogue  int8 rows times int8 weights, a scale a row and
+//                               a scale a column, bias, activation, residual
+//   ternary_gemm_s8_gated       int8 rows times the ternary weights of a gate and
+//                               of an up projection, act(g) u (64 rows and less
+//                               are multiplied in ternary_gemm.hip)
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "checks.h"
+#include "product.h"
+#include "ternary_gemm.h"
+
+namespace {
+
+namespace mm {
+template <int BM_, int BN_, int WM_, int WN_, int KS_, int D_, int PERCU_>
+struct Cfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KS = KS_, D = D_, PERCU = PERCU_;
+  static constexpr int NW = WM * WN, NT = 64 * NW, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  static constexpr int U = KS / 64, CH = KS / 16, RPL = 64 / CH;   // substeps, chunks a row, rows a wave's load
+  static constexpr int kAStage = BM * KS, kStage = (BM + BN) * KS, kLds = D * kStage;
+  static constexpr int kALoads = kAStage / 1024 / NW, kWLoads = BN * KS / 1024 / NW, kBatch = kALoads + kWLoads;
+  static constexpr int kWait = (D - 2) * kBatch;
+  static_assert(kALoads * 1024 * NW == kAStage && kWLoads * 1024 * NW == BN * KS, "whole loads");
+  static_assert(FM * 16 * WM == BM && FN * 16 * WN == BN && D >= 2 && kLds * PERCU <= 160 * 1024, "tile");
+  __host__ __device__ static constexpr int at(int r, int c) { return r * KS + 16 * (c ^ ((r >> 1) & (CH - 1))); }
+};
+}  // namespace mm
+
+struct MArgs {
+  const int8_t *A, *W;
+  Out o;
+  int64_t R, Cc, K;
+  int32_t tiles_r, tiles_c, tiles, band_cols, xcds;
+  int32_t nk;     // steps
+  int32_t tail;   // 16-byte chunks of the last step
+};
+
+template <class C, int E, bool BF>
+__global__ __attribute__((amdgpu_flat_work_group_size(C::NT, C::NT), amdgpu_waves_per_eu(C::NW * C::PERCU / 4)))
+void tgemm_int8(MArgs a) {
+  constexpr int FM = C::FM, FN = C::FN, D = C::D, U = C::U;
+  __shared__ __attribute__((aligned(1024))) int8_t smem[C::kLds];
+  const uint32_t lbase = (uint32_t)(uintptr_t)smem;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+
+  const int32_t nx = (int32_t)gridDim.x / a.xcds, xcd = (int32_t)blockIdx.x % a.xcds, j0 = (int32_t)blockIdx.x / a.xcds;
+  const int32_t q8 = a.tiles / a.xcds, r8 = a.tiles % a.xcds;
+  const int32_t start = xcd * q8 + (xcd < r8 ? xcd : r8) + j0, cnt = q8 + (xcd < r8 ? 1 : 0);
+  const int32_t ntile = cnt > j0 ? (cnt - j0 + nx - 1) / nx : 0;
+  if (ntile == 0) return;
+  auto tile_at = [&](int32_t it, int64_t &m0, int64_t &n0) {
+    int32_t tr, tc;
+    tile_rc(start + it * nx, a.tiles_r, a.tiles_c, a.band_cols, &tr, &tc);
+    m0 = (int64_t)tr * C::BM;
+    n0 = (int64_t)tc * C::BN;
+  };
+
+  uint32_t offA[C::kALoads], offW[C::kWLoads];
+  const int8_t *ab, *wb;
+  const int lrow = lane / C::CH, lslot = lane % C::CH;
+  auto set_loads = [&](int32_t it) {
+    int64_t m0, n0;
+    tile_at(it, m0, n0);
+    ab = a.A + m0 * a.K;
+    wb = a.W + n0 * a.K;
+    const int32_t mr = (int32_t)(a.R - m0 < C::BM ? a.R - m0 : C::BM) - 1, nr = (int32_t)(a.Cc - n0 < C::BN ? a.Cc - n0 : C::BN) - 1;
+#pragma unroll
+    for (int i = 0; i < C::kALoads; ++i) {
+      const int r = C::RPL * (C::kALoads * wave + i) + lrow;
+      offA[i] = (uint32_t)((r < mr ? r : mr) * (int32_t)a.K + 16 * (lslot ^ ((r >> 1) & (C::CH - 1))));
+    }
+#pragma unroll
+    for (int i = 0; i < C::kWLoads; ++i) {
+      const int r = C::RPL * (C::kWLoads * wave + i) + lrow;
+      offW[i] = (uint32_t)((r < nr ? r : nr) * (int32_t)a.K + 16 * (lslot ^ ((r >> 1) & (C::CH - 1))));
+    }
+  };
+  // the last step's chunks past the contraction load its last one again
+  auto clip_loads = [&]() {
+#pragma unroll
+    for (int i = 0; i < C::kALoads; ++i) {
+      const int c = lslot ^ (((C::RPL * (C::kALoads * wave + i) + lrow) >> 1) & (C::CH - 1));
+      if (c >= a.tail) offA[i] -= 16 * (uint32_t)(c - (a.tail - 1));
+    }
+#pragma unroll
+    for (int i = 0; i < C::kWLoads; ++i) {
+      const int c = lslot ^ (((C::RPL * (C::kWLoads * wave + i) + lrow) >> 1) & (C::CH - 1));
+      if (c >= a.tail) offW[i] -= 16 * (uint32_t)(c - (a.tail - 1));
+    }
+  };
+  auto load = [&](int i, int st, int32_t s) {
+    if (i < C::kALoads)
+      dma16(lbase + st * C::kStage + 1024 * (C::kALoads * wave + i), offA[i < C::kALoads ? i : 0], ab + C::KS * s);
+    else
+      dma16(lbase + st * C::kStage + C::kAStage + 1024 * (C::kWLoads * wave + i - C::kALoads),
+            offW[i >= C::kALoads ? i - C::kALoads : 0], wb + C::KS * s);
+  };
+  int32_t it_ld = 0, s_ld = 0;
+  auto next_load = [&]() {
+    if (s_ld + 1 < a.nk) {
+      ++s_ld;
+    } else if (it_ld + 1 < ntile) {
+      ++it_ld;
+      s_ld = 0;
+      set_loads(it_ld);
+    } else {
+      return;
+    }
+    if (s_ld == a.nk - 1 && a.tail != C::CH) clip_loads();
+  };
+  set_loads(0);
+  if (a.nk == 1 && a.tail != C::CH) clip_loads();
+#pragma unroll
+  for (int s = 0; s < D; ++s) {
+#pragma unroll
+    for (int i = 0; i < C::kBatch; ++i) load(i, s, s_ld);
+    next_load();
+  }
+  v4i acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int jj = 0; jj < FN; ++jj) acc[i][jj] = v4i{0, 0, 0, 0};
+
+  int qoff[U], poff[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    qoff[u] = wm * C::TM * C::KS + C::at(lane & 15, 4 * u + (lane >> 4));
+    poff[u] = C::kAStage + wn * C::TN * C::KS + C::at(lane & 15, 4 * u + (lane >> 4));
+  }
+  v4i q[2][FM], p[2][FN];
+  auto frag_q = [&](int st, int u, int i) { return *reinterpret_cast<const v4i *>(smem + st * C::kStage + qoff[u] + i * 16 * C::KS); };
+  auto frag_p = [&](int st, int u, int j) { return *reinterpret_cast<const v4i *>(smem + st * C::kStage + poff[u] + j * 16 * C::KS); };
+  wait_barrier<(D - 1) * C::kBatch>();
+#pragma unroll
+  for (int i = 0; i < FM; ++i) q[0][i] = frag_q(0, 0, i);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) p[0][j] = frag_p(0, 0, j);
+
+  constexpr int kStores = E & EPI_GATED ? FM * (BF || FN == 2 ? 1 : 2) : FM * (BF ? FN / 2 + FN % 2 : FN);
+  static_assert(C::kWait + kStores <= 63, "vmcnt field");
+  int st = 0, after = 0;
+  for (int32_t it = 0; it < ntile; ++it) {
+    for (int32_t s = 0; s < a.nk; ++s) {
+      const int st1 = st + 1 == D ? 0 : st + 1;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int cur = u & 1, nxt = U == 1 ? 0 : cur ^ 1;
+        constexpr int kBar = C::FM * 3 / 8;   // the slot that the barrier comes before
+        const int first = u == U - 1 ? kBar : 0, slots = FM - first;
+        v4i qn[FM], pn[FN];
+        // chunks of the last step past the contraction: A's count as zeros
+        if (s == a.nk - 1 && a.tail != C::CH && 4 * u + (lane >> 4) >= a.tail) {
+#pragma unroll
+          for (int i = 0; i < FM; ++i) q[cur][i] = v4i{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          if (u == U - 1 && i == kBar) {
+            if (after)
+              wait_barrier<C::kWait + kStores>();
+            else
+              wait_barrier<C::kWait>();
+            after = 0;
+          }
+          if (i >= first) {
+            const int k = i - first, sn = u + 1 < U ? st : st1, un = u + 1 < U ? u + 1 : 0;
+            // fragments of the next substep, the columns' first
+#pragma unroll
+            for (int x = k * (FM + FN) / slots; x < (k + 1) * (FM + FN) / slots; ++x) {
+              if (x < FN)
+                pn[x < FN ? x : 0] = frag_p(sn, un, x);
+              else
+                qn[x >= FN ? x - FN : 0] = frag_q(sn, un, x - FN);
+            }
+            if (u == U - 1) {
+#pragma unroll
+              for (int x = k * C::kBatch / slots; x < (k + 1) * C::kBatch / slots; ++x) load(x, st, s_ld);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(p[cur][j], q[cur][i], acc[i][j], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) q[nxt][i] = qn[i];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) p[nxt][j] = pn[j];
+      }
+      next_load();
+      st = st1;
+    }
+    int64_t m0, n0;
+    tile_at(it, m0, n0);
+    const int64_t r0 = m0 + wm * C::TM, c0 = n0 + wn * C::TN;
+    float rs[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int64_t row = r0 + (lane >> 2) + 16 * i;
+      rs[i] = a.o.rs[row < a.R ? row : a.R - 1];
+    }
+    const bool inside = m0 + C::BM <= a.R && n0 + C::BN <= a.Cc;
+    if constexpr (E & EPI_GATED) {
+      if (inside)
+        gated_tile<E, BF, false>(a.o, a.R, a.Cc / 2, acc, r0, c0 / 2, lane, rs);
+      else
+        gated_tile<E, BF, true>(a.o, a.R, a.Cc / 2, acc, r0, c0 / 2, lane, rs);
+    } else {
+      if (inside)
+        epi_tile<E, BF, false>(a.o, a.R, a.Cc, acc, r0, c0, lane, rs);
+      else
+        epi_tile<E, BF, true>(a.o, a.R, a.Cc, acc, r0, c0, lane, rs);
+    }
+    after = inside;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int jj = 0; jj < FN; ++jj) acc[i][jj] = v4i{0, 0, 0, 0};
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+
+// ---------------------------------------------------------------------------
+// Few rows (s8s8): the weights are nearly all of the bytes, and a workgroup of 8
+// waves owns 16 NB columns and 16 MF rows.  Its waves split the contraction into
+// super-steps of 256 (wave w takes w, w + 8, ...), operands straight into
+// registers a super-step ahead, and their sums meet in LDS, in wave order.
+// Lane l loads 16 bytes of row l % 16 at 64 q + 16 (l / 16), so that load q
+// takes 64 bytes of 16 rows, and q = 0 .. 3 are the four MFMA steps of the
+// super-step.  Any contraction and any alignment: loads are byte-aligned
+// vectors, and the last, partial super-step reads the bytes inside one by one.
+// ---------------------------------------------------------------------------
+namespace few {
+constexpr int kWaves = 8, kNT = 64 * kWaves, kStep = 256;
+}
+typedef int32_t v4i_u __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32_u __attribute__((aligned(1)));
+
+struct FewArgs {
+  const int8_t *A, *W;
+  Out o;
+  int64_t M, N, K;
+  int32_t rblocks;   // blocks of 16 MF rows
+  int32_t xcds;
+};
+
+// bytes 0 .. n - 1 of p, zeros past them
+__device__ __forceinline__ v4i load_part(const int8_t *p, int64_t n) {
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int b = 0; b < 16; ++b)
+    if (b < n) w[b >> 2] |= (uint32_t)(uint8_t)p[b] << (8 * (b & 3));
+  return v4i{(int32_t)w[0], (int32_t)w[1], (int32_t)w[2], (int32_t)w[3]};
+}
+
+template <int MF, int NB, int E>
+__global__ __attribute__((amdgpu_flat_work_group_size(few::kNT, few::kNT), amdgpu_waves_per_eu(2)))
+void int8_few(FewArgs a) {
+  using namespace few;
+  constexpr int kPitch = 4 * NB + 1, kWave = 16 * MF * kPitch;
+  __shared__ v4i red[kWaves * kWave];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  // an XCD's workgroups take neighbouring column blocks, the row blocks of one together
+  const int32_t pos = xcd_tile((int32_t)blockIdx.x, (int32_t)gridDim.x, a.xcds);
+  const int64_t n0 = (int64_t)(pos / a.rblocks) * 16 * NB, m0 = (int64_t)(pos % a.rblocks) * 16 * MF;
+  const int8_t *wr[NB], *ar[MF];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int64_t n = n0 + 16 * nb + r;
+    wr[nb] = a.W + (n < a.N ? n : a.N - 1) * a.K + 16 * g;
+  }
+#pragma unroll
+  for (int mf = 0; mf < MF; ++mf) {
+    const int64_t m = m0 + 16 * mf + r;
+    ar[mf] = a.A + (m < a.M ? m : a.M - 1) * a.K + 16 * g;
+  }
+  v4i acc[MF][NB];
+#pragma unroll
+  for (int mf = 0; mf < MF; ++mf)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) acc[mf][nb] = v4i{0, 0, 0, 0};
+  typedef v4i W4[NB][4];
+  typedef v4i A4[MF][4];
+  auto load = [&](W4 &w, A4 &x, int64_t k) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) w[nb][q] = *reinterpret_cast<const v4i_u *>(wr[nb] + k + 64 * q);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int mf = 0; mf < MF; ++mf) x[mf][q] = *reinterpret_cast<const v4i_u *>(ar[mf] + k + 64 * q);
+  };
+  auto step = [&](const W4 &w, const A4 &x) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int mf = 0; mf < MF; ++mf)
+          acc[mf][nb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[nb][q], x[mf][q], acc[mf][nb], 0, 0, 0);
+  };
+  const int32_t nfull = (int32_t)(a.K / kStep), cnt = nfull > wave ? (nfull - wave + kWaves - 1) / kWaves : 0;
+  if (cnt > 0) {
+    W4 w0, w1;
+    A4 x0, x1;
+    const int32_t last = wave + kWaves * (cnt - 1);   // past it the loads repeat it: in range, never used
+    load(w0, x0, (int64_t)kStep * wave);
+    int32_t s = wave;
+    for (int32_t i = 0; i + 2 <= cnt; i += 2) {
+      const int32_t s1 = s + kWaves, s2 = s1 + kWaves < last ? s1 + kWaves : last;
+      load(w1, x1, (int64_t)kStep * s1);
+      __builtin_amdgcn_sched_barrier(0);   // the loads ahead of the products
+      step(w0, x0);
+      load(w0, x0, (int64_t)kStep * s2);
+      __builtin_amdgcn_sched_barrier(0);
+      step(w1, x1);
+      s += 2 * kWaves;
+    }
+    if (cnt & 1) step(w0, x0);
+  }
+  if (a.K % kStep != 0 && wave == nfull % kWaves) {
+    const int64_t k = (int64_t)kStep * nfull;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      const int64_t at = k + 64 * q, n = a.K - at - 16 * g;   // bytes of this lane's chunk inside
+      if (at >= a.K) break;
+      v4i w[NB], x[MF];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) w[nb] = n >= 16 ? v4i(*reinterpret_cast<const v4i_u *>(wr[nb] + at)) : load_part(wr[nb] + at, n);
+#pragma unroll
+      for (int mf = 0; mf < MF; ++mf) x[mf] = n >= 16 ? v4i(*reinterpret_cast<const v4i_u *>(ar[mf] + at)) : load_part(ar[mf] + at, n);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int mf = 0; mf < MF; ++mf)
+          acc[mf][nb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[nb], x[mf], acc[mf][nb], 0, 0, 0);
+    }
+  }
+  v4i *mine = red + wave * kWave;
+#pragma unroll
+  for (int mf = 0; mf < MF; ++mf)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) mine[(16 * mf + r) * kPitch + 4 * nb + g] = acc[mf][nb];
+  __syncthreads();
+  constexpr int kQuads = 4 * NB, kOut = 16 * MF * kQuads;
+  static_assert(kOut <= kNT, "a quad a thread");
+  if (tid >= kOut) return;
+  const int m = tid / kQuads, cq = tid % kQuads;
+  v4i sum = red[m * kPitch + cq];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) sum += red[w * kWave + m * kPitch + cq];
+  const int64_t row = m0 + m, col = n0 + 4 * cq;
+  if (row >= a.M) return;
+  const float rs = a.o.rs[row];
+  if (col + 3 < a.N) {
+    epi_put4<E>(a.o, a.N, row, col, sum, rs);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < a.N) epi_put1<E>(a.o, a.N, row, col + e, sum[e], rs);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows laid out for tgemm_int8, a wave a row, 16 bytes a lane: as they are, with
+// a length that is whole 16-byte chunks (zeros past the contraction), or decoded
+// from stored codes, a gate's row and an up projection's in turn.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void lay_rows(const int8_t *__restrict__ src, int8_t *__restrict__ dst, int64_t R,
+                                                int64_t K, int64_t Kp) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= R) return;
+  const int8_t *p = src + row * K;
+  v4i *q = reinterpret_cast<v4i *>(dst + row * Kp);
+  for (int64_t c = threadIdx.x & 63; c < Kp / 16; c += 64) {
+    const int64_t n = K - 16 * c;
+    q[c] = n >= 16 ? v4i(*reinterpret_cast<const v4i_u *>(p + 16 * c)) : load_part(p + 16 * c, n);
+  }
+}
+__global__ __launch_bounds__(256) void lay_gated(const uint8_t *__restrict__ src, int8_t *__restrict__ dst, int64_t N,
+                                                 int64_t K, int64_t Kp) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= 2 * N) return;
+  const uint8_t *p = src + ((row & 1) * N + (row >> 1)) * (K / 4);
+  v4i *q = reinterpret_cast<v4i *>(dst + row * Kp);
+  for (int64_t c = threadIdx.x & 63; c < Kp / 16; c += 64) {
+    const int64_t n = K / 4 - 4 * c;
+    uint32_t x = 0;
+    if (n >= 4) {
+      x = *reinterpret_cast<const u32_u *>(p + 4 * c);
+    } else {
+#pragma unroll
+      for (int b = 0; b < 3; ++b)
+        if (b < n) x |= (uint32_t)p[4 * c + b] << (8 * b);
+    }
+    q[c] = decode16(x);   // code 0 is weight 0
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+struct Machine {
+  int32_t cus, xcds;
+};
+
+int64_t align_of(const void *p) {
+  const uintptr_t v = (uintptr_t)p;
+  return v ? (int64_t)(v & (~v + 1)) : 1 << 20;
+}
+int64_t min_align(int64_t a, int64_t b) { return a < b ? a : b; }
+int64_t round_up(int64_t v, int64_t n) { return ceil_div(v, n) * n; }
+
+bool mul_ok(int64_t a, int64_t b, int64_t *out) {
+  if (b > INT64_MAX / a) return false;
+  *out = a * b;
+  return true;
+}
+int check_sizes(int64_t M, int64_t N, int64_t K) {
+  int64_t t;
+  if (M < 1 || N < 1 || K < 1) return TGEMM_ERR_DIM;
+  // every byte count (two float32 matrices side by side at most) fits, and so do the tiles
+  if (!mul_ok(M, K, &t) || !mul_ok(t, 8, &t) || !mul_ok(N, K, &t) || !mul_ok(t, 8, &t) || !mul_ok(M, N, &t) ||
+      !mul_ok(t, 8, &t))
+    return TGEMM_ERR_DIM;
+  if (M > INT64_MAX / 2 / 64 || N > INT32_MAX || ceil_div(M, 16) * ceil_div(2 * N, 16) > INT32_MAX) return TGEMM_ERR_DIM;
+  return TGEMM_OK;
+}
+
+typedef mm::Cfg<256, 128, 4, 2, 128, 3, 1> Large;
+typedef mm::Cfg<128, 128, 2, 2, 128, 2, 2> Mid;
+typedef mm::Cfg<64, 128, 2, 2, 128, 3, 2> Small;
+typedef mm::Cfg<64, 64, 2, 2, 128, 4, 2> Tiny;
+
+template <class C, int E>
+int launch_mm(MArgs a, const Machine &mc, hipStream_t stream) {
+  a.tiles_r = (int32_t)ceil_div(a.R, C::BM);
+  a.tiles_c = (int32_t)ceil_div(a.Cc, C::BN);
+  a.tiles = a.tiles_r * a.tiles_c;
+  a.xcds = mc.xcds;
+  a.band_cols = a.tiles_c < 4 ? a.tiles_c : 4;
+  a.nk = (int32_t)ceil_div(a.K, C::KS);
+  a.tail = (int32_t)((a.K - (int64_t)(a.nk - 1) * C::KS) / 16);
+  int64_t grid = (int64_t)mc.cus * C::PERCU;
+  if (a.tiles < grid) grid = round_up(a.tiles, mc.xcds);
+  if (a.o.kind == OUT_BF16)
+    hipLaunchKernelGGL((tgemm_int8<C, E, true>), dim3((unsigned)grid), dim3(C::NT), 0, stream, a);
+  else
+    hipLaunchKernelGGL((tgemm_int8<C, E, false>), dim3((unsigned)grid), dim3(C::NT), 0, stream, a);
+  return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
+}
+template <class C>
+int64_t rounds(int64_t R, int64_t Cc, const Machine &mc) {
+  return ceil_div(ceil_div(R, C::BM) * ceil_div(Cc, C::BN), (int64_t)mc.cus * C::PERCU);
+}
+template <int E>
+int pick_mm(const MArgs &a, const Machine &mc, hipStream_t stream) {
+  if (ceil_div(a.R, 128) * ceil_div(a.Cc, 128) <= mc.cus / 2) return launch_mm<Tiny, E>(a, mc, stream);
+  if (ceil_div(a.R, 128) * ceil_div(a.Cc, 128) <= mc.cus) return launch_mm<Small, E>(a, mc, stream);
+  if (ceil_div(a.R, 256) * ceil_div(a.Cc, 128) < mc.cus) return launch_mm<Mid, E>(a, mc, stream);
+  return launch_mm<Large, E>(a, mc, stream);
+}
+template <int FLAG>
+int pick_mm_act(const MArgs &a, const Machine &mc, hipStream_t stream) {
+  return epi_of(a.o.act) == EPI_POLY ? pick_mm<EPI_POLY | FLAG>(a, mc, stream) : pick_mm<EPI_SIGM | FLAG>(a, mc, stream);
+}
+
+void lay(const int8_t *src, int8_t *dst, int64_t R, int64_t K, int64_t Kp, hipStream_t stream) {
+  hipLaunchKernelGGL(lay_rows, dim3((unsigned)ceil_div(R, 4)), dim3(256), 0, stream, src, dst, R, K, Kp);
+}
+
+// few rows go to int8_few, which needs no layout
+constexpr int64_t kFewRows = 64;
+
+// the workspace of a call: the rows of either operand laid out anew where they
+// are not whole, aligned 16-byte chunks, those of the gated product's weights always
+struct Layout {
+  int64_t kp, a_bytes, w_bytes;
+};
+Layout layout_of(int64_t M, int64_t rows, int64_t K, bool lay_a, bool lay_w) {
+  Layout l;
+  l.kp = round_up(K, 16);
+  l.a_bytes = lay_a ? round_up(M * l.kp, 256) : 0;
+  l.w_bytes = lay_w ? rows * l.kp : 0;
+  return l;
+}
+Layout s8s8_layout(int64_t M, int64_t N, int64_t K, int64_t a_align, int64_t w_align) {
+  const bool few = M <= kFewRows, odd = K % 16 != 0;
+  return layout_of(M, N, K, !few && (odd || a_align % 16 != 0), !few && (odd || w_align % 16 != 0));
+}
+Layout gated_layout(int64_t M, int64_t N, int64_t K, int64_t a_align, int64_t w_align) {
+  const bool few = gated_few_ok(M, N, K, min_align(a_align, w_align));
+  return layout_of(M, 2 * N, K, !few && (K % 16 != 0 || a_align % 16 != 0), !few);
+}
+
+template <int MF, int NB, int E>
+int launch_few_e(FewArgs a, hipStream_t stream) {
+  a.rblocks = (int32_t)ceil_div(a.M, 16 * MF);
+  hipLaunchKernelGGL((int8_few<MF, NB, E>), dim3((unsigned)(ceil_div(a.N, 16 * NB) * a.rblocks)), dim3(few::kNT), 0,
+                     stream, a);
+  return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
+}
+template <int MF, int NB>
+int launch_few(const FewArgs &a, hipStream_t stream) {
+  return epi_of(a.o.act) == EPI_POLY ? launch_few_e<MF, NB, EPI_POLY | EPI_COLS>(a, stream)
+                                     : launch_few_e<MF, NB, EPI_SIGM | EPI_COLS>(a, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int ternary_gemm_s8s8_workspace(int64_t M, int64_t N, int64_t K, int64_t align, int64_t *bytes) {
+  if (!bytes) return TGEMM_ERR_NULL;
+  const int st = check_sizes(M, N, K);
+  if (st != TGEMM_OK) return st;
+  if (K > TGEMM_INT8_MAX_CONTRACTION) return TGEMM_ERR_BOUND;
+  const Layout l = s8s8_layout(M, N, K, align > 0 ? align : 1, align > 0 ? align : 1);
+  *bytes = l.a_bytes + l.w_bytes;
+  return TGEMM_OK;
+}
+
+int ternary_gemm_s8s8_epilogue(const int8_t *A, const int8_t *W, const float *a_row_scale, const float *w_col_scale,
+                               const float *bias, int act, const void *residual, void *Y, void *Z, int out_kind,
+                               int64_t M, int64_t N, int64_t K, void *workspace, int64_t workspace_bytes,
+                               hipStream_t stream) {
+  if (!A || !W || !a_row_scale || !Y) return TGEMM_ERR_NULL;
+  if (out_kind != TGEMM_OUT_F32 && out_kind != TGEMM_OUT_BF16) return TGEMM_ERR_KIND;
+  if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_VALUE;
+  const int st = check_sizes(M, N, K);
+  if (st != TGEMM_OK) return st;
+  if (K > TGEMM_INT8_MAX_CONTRACTION) return TGEMM_ERR_BOUND;
+  const Layout l = s8s8_layout(M, N, K, align_of(A), align_of(W));
+  if (!workspace_ok(workspace, workspace_bytes, l.a_bytes + l.w_bytes)) return TGEMM_ERR_WORKSPACE;
+  const int64_t ob = M * N * (out_kind == TGEMM_OUT_F32 ? 4 : 2);
+  const Buf outs[] = {{Y, ob}, {Z, ob}, {workspace, workspace_bytes > 0 ? workspace_bytes : 0}};
+  const Buf ins[] = {{A, M * K}, {W, N * K}, {a_row_scale, 4 * M}, {w_col_scale, 4 * N}, {bias, 4 * N}, {residual, ob}};
+  const void *const same[3][2] = {{residual, residual}};
+  if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
+  Machine mc;
+  if (ternary_gemm_machine(&mc.cus, &mc.xcds) != TGEMM_OK) return TGEMM_ERR_HIP;
+  Out o{};
+  o.ptr = Y;
+  o.rs = a_row_scale;
+  o.cs = w_col_scale;
+  o.cscal = 1.f;
+  o.kind = out_kind;
+  o.bias = bias;
+  o.res = residual;
+  o.z = Z;
+  o.act = act;
+  if (M <= kFewRows) {
+    const FewArgs a = {A, W, o, M, N, K, 0, mc.xcds};
+    const int64_t half = mc.cus / 2;
+    if (M <= 16) {
+      if (N >= 64 * half) return launch_few<1, 4>(a, stream);
+      return N >= 32 * half ? launch_few<1, 2>(a, stream) : launch_few<1, 1>(a, stream);
+    }
+    if (N >= 64 * half) return launch_few<2, 4>(a, stream);
+    return N >= 32 * half ? launch_few<2, 2>(a, stream) : launch_few<2, 1>(a, stream);
+  }
+  int8_t *la = static_cast<int8_t *>(workspace), *lw = la + l.a_bytes;
+  if (l.a_bytes) lay(A, la, M, K, l.kp, stream);
+  if (l.w_bytes) lay(W, lw, N, K, l.kp, stream);
+  const MArgs a = {l.a_bytes ? la : A, l.w_bytes ? lw : W, o, M, N, l.kp, 0, 0, 0, 0, 0, 0, 0};
+  return pick_mm_act<EPI_COLS>(a, mc, stream);
+}
+
+int ternary_gemm_s8_gated_workspace(int64_t M, int64_t N, int64_t K, int64_t align, int64_t *bytes) {
+  if (!bytes) return TGEMM_ERR_NULL;
+  const int st = check_sizes(M, N, K);
+  if (st != TGEMM_OK) return st;
+  if (K % 4 != 0) return TGEMM_ERR_PACK;
+  if (K > TGEMM_TERNARY_MAX_CONTRACTION) return TGEMM_ERR_BOUND;
+  const Layout l = gated_layout(M, N, K, align > 0 ? align : 1, align > 0 ? align : 1);
+  *bytes = l.a_bytes + l.w_bytes;
+  return TGEMM_OK;
+}
+
+int ternary_gemm_s8_gated(const int8_t *A, const uint8_t *Wpacked, const float *a_row_scale, float gate_scale,
+                          float up_scale, const float *bias, int act, void *Y, void *Z, int out_kind, int64_t M, int64_t N,
+                          int64_t K, void *workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (!A || !Wpacked || !a_row_scale || !Y) return TGEMM_ERR_NULL;
+  if (out_kind != TGEMM_OUT_F32 && out_kind != TGEMM_OUT_BF16) return TGEMM_ERR_KIND;
+  if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_VALUE;
+  const int st = check_sizes(M, N, K);
+  if (st != TGEMM_OK) return st;
+  if (K % 4 != 0) return TGEMM_ERR_PACK;
+  if (K > TGEMM_TERNARY_MAX_CONTRACTION) return TGEMM_ERR_BOUND;
+  const Layout l = gated_layout(M, N, K, align_of(A), align_of(Wpacked));
+  if (!workspace_ok(workspace, workspace_bytes, l.a_bytes + l.w_bytes)) return TGEMM_ERR_WORKSPACE;
+  const int64_t ob = M * N * (out_kind == TGEMM_OUT_F32 ? 4 : 2);
+  const Buf outs[] = {{Y, ob}, {Z, 2 * ob}, {workspace, workspace_bytes > 0 ? workspace_bytes : 0}};
+  const Buf ins[] = {{A, M * K}, {Wpacked, 2 * N * (K / 4)}, {a_row_scale, 4 * M}, {bias, 8 * N}};
+  const void *const same[3][2] = {};
+  if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
+  Machine mc;
+  if (ternary_gemm_machine(&mc.cus, &mc.xcds) != TGEMM_OK) return TGEMM_ERR_HIP;
+  if (!l.w_bytes)
+    return gated_few({A, Wpacked, a_row_scale, bias, gate_scale, up_scale, Y, Z, out_kind, act, M, N, K}, mc.cus, mc.xcds,
+                     stream);
+  int8_t *la = static_cast<int8_t *>(workspace), *lw = la + l.a_bytes;
+  if (l.a_bytes) lay(A, la, M, K, l.kp, stream);
+  hipLaunchKernelGGL(lay_gated, dim3((unsigned)ceil_div(2 * N, 4)), dim3(256), 0, stream, Wpacked, lw, N, K, l.kp);
+  Out o{};
+  o.ptr = Y;
+  o.rs = a_row_scale;
+  o.cscal = gate_scale;
+  o.cscal2 = up_scale;
+  o.kind = out_kind;
+  o.bias = bias;
+  o.z = Z;
+  o.act = act;
+  const MArgs a = {l.a_bytes ? la : A, lw, o, M, 2 * N, l.kp, 0, 0, 0, 0, 0, 0, 0};
+  return pick_mm_act<EPI_GATED>(a, mc, stream);
+}
+
+}  // extern "C"

@@ -1822,7 +1822,9 @@ __device__ __forceinline__ void sk_epilogue(int8_t *smem, const v4i (&acc)[MF][N
     const int32_t col = c0 + 4 * cq;
     if (m < M) {
       const float rsc = row_scale(o, m);
-      if (o.vec && col + 3 < width) {
+      if constexpr (E & EPI_GATED) {
+        gated_put<E>(o, width / 2, m, col / 2, sum, rsc);
+      } else if (o.vec && col + 3 < width) {
         put4<E>(o, width, m, col, sum, rsc);
       } else {
 #pragma unroll
@@ -1844,12 +1846,22 @@ void tgemm_skinny(KArgs a) {
   // column block in the XCD-contiguous order (as the skinny dX kernel)
   const int32_t n0 = xcd_tile((int32_t)blockIdx.x, (int32_t)gridDim.x, a.xcds) * 16 * NB;
   const int64_t kb = a.K / 4;
+  if constexpr (E & EPI_GATED) {   // rows 16 MF blockIdx.y .. of the output
+    const int64_t r0 = 16 * MF * (int64_t)blockIdx.y, esz = a.o.kind == OUT_F32 ? 4 : 2;
+    a.A += r0 * a.K;
+    a.M -= (int32_t)r0;
+    a.o.rs += r0;
+    a.o.ptr = static_cast<char *>(a.o.ptr) + r0 * (a.N / 2) * esz;
+    if (a.o.z) a.o.z = static_cast<char *>(a.o.z) + r0 * a.N * esz;
+  }
 
   const uint8_t *wr[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const int32_t n = n0 + 16 * nb + r;
-    wr[nb] = a.Wp + (int64_t)(n < a.N ? n : a.N - 1) * kb + 16 * g;
+    int32_t n = n0 + 16 * nb + r;
+    n = n < a.N ? n : a.N - 1;
+    if constexpr (E & EPI_GATED) n = (n & 1) * (a.N / 2) + (n >> 1);   // the gate's weights, then the up projection's
+    wr[nb] = a.Wp + (int64_t)n * kb + 16 * g;
   }
   typename SkA<MF, AL>::Ptr ar;
 #pragma unroll
@@ -2792,7 +2804,55 @@ int fill_plan(int op, bool epi, int64_t M, int64_t N, int64_t K, int64_t align, 
   return TGEMM_OK;
 }
 
+// The gated product of few rows, on the stored codes: the skinny forward's
+// kernels over column pairs, blocks of 32 rows side by side.
+template <int MF, int NB, bool AL>
+void launch_gated_few(const KArgs &ka, dim3 grid, hipStream_t stream) {
+  if (epi_of(ka.o.act) == EPI_POLY)
+    hipLaunchKernelGGL((tgemm_skinny<MF, NB, AL, EPI_POLY | EPI_GATED>), grid, dim3(sk::kNT), 0, stream, ka);
+  else
+    hipLaunchKernelGGL((tgemm_skinny<MF, NB, AL, EPI_SIGM | EPI_GATED>), grid, dim3(sk::kNT), 0, stream, ka);
+}
+
 }  // namespace
+
+bool gated_few_ok(int64_t M, int64_t N, int64_t K, int64_t align) {
+  return M <= kGatedFewRows && K % 64 == 0 && align % 16 == 0 && N <= (INT32_MAX - 64) / 2 && K <= INT32_MAX;
+}
+
+int gated_few(const GatedCall &c, int32_t cus, int32_t xcds, hipStream_t stream) {
+  const SkinnyPlan kp = skinny_plan(FWD, c.M < 32 ? c.M : 32, 2 * c.N, c.K, 16, 16, {cus, xcds});
+  KArgs ka{};
+  ka.xcds = xcds;
+  ka.A = c.A;
+  ka.Wp = c.Wpacked;
+  ka.o.ptr = c.Y;
+  ka.o.z = c.Z;
+  ka.o.rs = c.row_scale;
+  ka.o.cscal = c.gate_scale;
+  ka.o.cscal2 = c.up_scale;
+  ka.o.bias = c.bias;
+  ka.o.kind = c.kind;
+  ka.o.act = c.act;
+  ka.M = (int32_t)c.M;
+  ka.N = (int32_t)(2 * c.N);
+  ka.K = (int32_t)c.K;
+  ka.nfull = (int32_t)(c.K / sk::SK);
+  ka.vq = (int32_t)(c.K % sk::SK / BK);
+  const dim3 grid((unsigned)kp.grid, (unsigned)ceil_div(c.M, 32));
+  switch (100 * kp.mf + 10 * kp.nb + (kp.al ? 1 : 0)) {
+    case 110: launch_gated_few<1, 1, false>(ka, grid, stream); break;
+    case 120: launch_gated_few<1, 2, false>(ka, grid, stream); break;
+    case 140: launch_gated_few<1, 4, false>(ka, grid, stream); break;
+    case 111: launch_gated_few<1, 1, true>(ka, grid, stream); break;
+    case 121: launch_gated_few<1, 2, true>(ka, grid, stream); break;
+    case 141: launch_gated_few<1, 4, true>(ka, grid, stream); break;
+    case 211: launch_gated_few<2, 1, true>(ka, grid, stream); break;
+    case 221: launch_gated_few<2, 2, true>(ka, grid, stream); break;
+    default: launch_gated_few<2, 4, true>(ka, grid, stream); break;
+  }
+  return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
+}
 
 extern "C" {
 
