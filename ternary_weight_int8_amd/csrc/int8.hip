@@ -25,10 +25,18 @@ struct Cfg {
   static constexpr int kALoads = kAStage / 1024 / NW, kWLoads = BN * KS / 1024 / NW, kBatch = kALoads + kWLoads;
   static constexpr int kWait = (D - 2) * kBatch;
   static_assert(kALoads * 1024 * NW == kAStage && kWLoads * 1024 * NW == BN * KS, "whole loads");
-  static_assert(FM * 16 * WM == BM && FN * 16 * WN == BN && D >= 2 && kLds * PERCU <= 160 * 1024, "tile");
+  // scales and biases of a tile's rows and columns, in 64-lane loads
+  static constexpr int kAux = BM / 64 + 2 * (BN / 64), kAuxLoads = (kAux + NW - 1) / NW, kAuxBytes = 256 * kAux;
+  static_assert(FM * 16 * WM == BM && FN * 16 * WN == BN && BM % 64 == 0 && BN % 64 == 0 && D >= 2, "tile");
+  static_assert((kLds + kAuxBytes) * PERCU <= 160 * 1024, "LDS");
   __host__ __device__ static constexpr int at(int r, int c) { return r * KS + 16 * (c ^ ((r >> 1) & (CH - 1))); }
 };
 }  // namespace mm
+
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
 
 struct MArgs {
   const int8_t *A, *W;
@@ -39,11 +47,254 @@ struct MArgs {
   int32_t tail;   // 16-byte chunks of the last step
 };
 
+// ---------------------------------------------------------------------------
+// A tile's output.  Scales and biases come from LDS, where the tile's loads have
+// put them: a global load here would wait for the stores before it, since a
+// wave's memory operations complete in order (with such loads the end of a 256 x
+// 128 tile took 6 us, and 16384x6912x1280 bf16 187 us).  For the same reason a residual
+// is read a fragment row ahead, before the stores of the row in hand.
+//   aux: BM row scales, then BN column scales (COLS) or nothing, then BN biases
+// A fragment row goes out as in epi_run: bfloat16 fragments in pairs, 16 bytes a
+// lane, four lanes 64 bytes of a row; float32 16 bytes a lane, 64 a row.
+// ---------------------------------------------------------------------------
+template <class C, int E, bool BF, bool GUARD>
+struct PlainOut {
+  static constexpr int FM = C::FM, FN = C::FN, kKind = BF ? OUT_BF16 : OUT_F32;
+  static_assert(FN % 2 == 0, "pairs of fragments");
+  const Out &o;
+  const float *aux;        // LDS
+  int64_t R, N, r0, c0;    // the output, the wave's first row and column
+  int rl, cl;              // the same in the tile
+  int lane;
+
+  __device__ __forceinline__ int col_of(int jj) const {   // of the wave's columns: the first of register set jj
+    const int p = lane & 3;
+    return BF ? 32 * (jj / 2) + 8 * p + 4 * (jj & 1) : 16 * jj + 4 * p;
+  }
+  __device__ __forceinline__ void load_res(float (&x)[FN][4], int i) const {
+    int64_t row = r0 + (lane >> 2) + 16 * i;
+    if (GUARD && row >= R) row = R - 1;
+#pragma unroll
+    for (int jj = 0; jj < FN; ++jj) {
+      const int64_t col = c0 + col_of(jj), at = row * N + col;
+      if (!GUARD || col + 3 < N) {
+        if constexpr (BF) {
+          const v2u_u v = *reinterpret_cast<const v2u_u *>(static_cast<const uint16_t *>(o.res) + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[jj][e] = __uint_as_float(e & 1 ? v[e / 2] & 0xFFFF0000u : v[e / 2] << 16);
+        } else {
+          const v4f_u v = *reinterpret_cast<const v4f_u *>(static_cast<const float *>(o.res) + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[jj][e] = v[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t in = row * N + (col + e < N ? col + e : N - 1);   // past the row its last element, never stored
+          x[jj][e] = BF ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(o.res)[in] << 16)
+                        : static_cast<const float *>(o.res)[in];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(void *base, const float (&y)[FN][4], int i) const {
+    const int64_t row = r0 + (lane >> 2) + 16 * i;
+    if (GUARD && row >= R) return;
+#pragma unroll
+    for (int jj = 0; jj < FN; ++jj) {
+      const int64_t col = c0 + col_of(jj), at = row * N + col;
+      if (BF && !(jj & 1) && (!GUARD || col + 7 < N)) {
+        *reinterpret_cast<v4u_u *>(static_cast<uint16_t *>(base) + at) =
+            v4u_u{bf16_pack(y[jj][0], y[jj][1]), bf16_pack(y[jj][2], y[jj][3]), bf16_pack(y[jj | 1][0], y[jj | 1][1]),
+                  bf16_pack(y[jj | 1][2], y[jj | 1][3])};
+      } else if (BF && (jj & 1) && (!GUARD || col + 3 < N)) {
+        // went with the set before it
+      } else if (!GUARD || col + 3 < N) {
+        store4(base, kKind, at, y[jj]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < N) store1(base, kKind, at + e, y[jj][e]);
+      }
+    }
+  }
+  __device__ __forceinline__ void run(const v4i (&acc)[FM][FN]) const {
+#pragma clang fp contract(off)   // every kernel rounds alike
+    const int p = lane & 3, src = 4 * ((lane >> 2) + 16 * p);
+    const float *cs = aux + C::BM + cl, *bias = cs + C::BN;
+    float res[2][FN][4];
+    if (o.res) load_res(res[0], 0);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (o.res && i + 1 < FM) load_res(res[(i + 1) & 1], i + 1);
+      const float rs = aux[rl + (lane >> 2) + 16 * i];
+      float y[FN][4];
+      {
+        v4i v[FN];
+#pragma unroll
+        for (int jj = 0; jj < FN; ++jj) v[jj] = acc[i][jj];
+        if constexpr (BF) {
+#pragma unroll
+          for (int k = 0; k < FN; k += 2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const auto h = __builtin_amdgcn_permlane32_swap(v[k][e], v[k + 1][e], false, false);
+              const auto q = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+              v[k][e] = q[0];
+              v[k + 1][e] = q[1];
+            }
+        }
+#pragma unroll
+        for (int jj = 0; jj < FN; ++jj)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[jj][e] = __fmul_rn((float)__builtin_amdgcn_ds_bpermute(src, v[jj][e]), rs);
+      }
+      if (o.cs) {
+#pragma unroll
+        for (int jj = 0; jj < FN; ++jj) {
+          const float4 c = *reinterpret_cast<const float4 *>(cs + col_of(jj));
+          y[jj][0] *= c.x;
+          y[jj][1] *= c.y;
+          y[jj][2] *= c.z;
+          y[jj][3] *= c.w;
+        }
+      }
+      if (o.bias) {
+#pragma unroll
+        for (int jj = 0; jj < FN; ++jj) {
+          const float4 b = *reinterpret_cast<const float4 *>(bias + col_of(jj));
+          y[jj][0] += b.x;
+          y[jj][1] += b.y;
+          y[jj][2] += b.z;
+          y[jj][3] += b.w;
+        }
+      }
+      if (o.z) store(o.z, y, i);
+      if ((E & kEpiAct) != EPI_POLY || o.act != TGEMM_ACT_NONE) {
+#pragma unroll
+        for (int jj = 0; jj < FN; ++jj)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[jj][e] = epi_act<E>(y[jj][e], o.act);
+      }
+      if (o.res) {
+#pragma unroll
+        for (int jj = 0; jj < FN; ++jj)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[jj][e] += res[i & 1][jj][e];
+      }
+      store(o.ptr, y, i);
+      __builtin_amdgcn_sched_barrier(0);   // the next row's registers do not mix with this one's
+    }
+  }
+};
+
+// The same for column pairs (gated): lane groups and registers are exchanged
+// (permlane swaps) until group p of 16 lanes holds 4 FN neighbouring columns, and
+// ds_bpermute then gives four neighbouring lanes a row: a lane has 2 FN
+// neighbouring outputs, and a row's four lanes 8 FN.
+//   aux: BM row scales, BN of nothing, BN / 2 biases of the gate, BN / 2 of the up projection
+template <class C, int E, bool BF, bool GUARD>
+struct GatedOut {
+  static constexpr int FM = C::FM, FN = C::FN, kKind = BF ? OUT_BF16 : OUT_F32, kOut = 2 * FN;
+  static_assert(FN == 2 || FN == 4, "pairs or fours of fragments");
+  const Out &o;
+  const float *aux;
+  int64_t R, N, r0, c0;    // N, c0 and cl count outputs
+  int rl, cl;
+  int lane;
+
+  __device__ __forceinline__ void store(void *base, int64_t at, int64_t col, const float (&y)[kOut]) const {
+    if (!GUARD || col + kOut <= N) {
+      if constexpr (BF && kOut == 8) {
+        *reinterpret_cast<v4u_u *>(static_cast<uint16_t *>(base) + at) =
+            v4u_u{bf16_pack(y[0], y[1]), bf16_pack(y[2], y[3]), bf16_pack(y[4], y[5]), bf16_pack(y[6], y[7])};
+      } else {
+#pragma unroll
+        for (int k = 0; k < kOut; k += 4) store4(base, kKind, at + k, {y[k], y[k + 1], y[k + 2], y[k + 3]});
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kOut; ++k)
+        if (col + k < N) store1(base, kKind, at + k, y[k]);
+    }
+  }
+  __device__ __forceinline__ void run(const v4i (&acc)[FM][FN]) const {
+#pragma clang fp contract(off)   // every kernel rounds alike
+    const int p = lane & 3, src = 4 * ((lane >> 2) + 16 * p);
+    const float *bias = aux + C::BM + C::BN + cl + kOut * p;
+    const int64_t col = c0 + kOut * p;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int64_t row = r0 + (lane >> 2) + 16 * i;
+      const float rs = aux[rl + (lane >> 2) + 16 * i];
+      float g[kOut], u[kOut];
+      {
+        v4i v[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) v[j] = acc[i][j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (FN == 4) {
+            const auto a = __builtin_amdgcn_permlane32_swap(v[0][e], v[2][e], false, false);
+            const auto b = __builtin_amdgcn_permlane32_swap(v[1][e], v[3][e], false, false);
+            const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+            const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+            v[0][e] = c[0];
+            v[1][e] = c[1];
+            v[2][e] = d[0];
+            v[3][e] = d[1];
+          } else {
+            const auto a = __builtin_amdgcn_permlane32_swap(v[0][e], v[1][e], false, false);
+            const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[1], false, false);
+            v[0][e] = b[0];
+            v[1][e] = b[1];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            g[2 * j + e] = scaled(__builtin_amdgcn_ds_bpermute(src, v[j][2 * e]), rs, o.cscal);
+            u[2 * j + e] = scaled(__builtin_amdgcn_ds_bpermute(src, v[j][2 * e + 1]), rs, o.cscal2);
+          }
+      }
+      if (o.bias) {
+#pragma unroll
+        for (int k = 0; k < kOut; k += 4) {
+          const float4 a = *reinterpret_cast<const float4 *>(bias + k), b = *reinterpret_cast<const float4 *>(bias + C::BN / 2 + k);
+          g[k] += a.x;
+          g[k + 1] += a.y;
+          g[k + 2] += a.z;
+          g[k + 3] += a.w;
+          u[k] += b.x;
+          u[k + 1] += b.y;
+          u[k + 2] += b.z;
+          u[k + 3] += b.w;
+        }
+      }
+      const bool in = !GUARD || row < R;
+      if (o.z && in) {
+        store(o.z, 2 * row * N + col, col, g);
+        store(o.z, (2 * row + 1) * N + col, col, u);
+      }
+      if ((E & kEpiAct) != EPI_POLY || o.act != TGEMM_ACT_NONE) {
+#pragma unroll
+        for (int k = 0; k < kOut; ++k) g[k] = epi_act<E>(g[k], o.act);
+      }
+#pragma unroll
+      for (int k = 0; k < kOut; ++k) g[k] *= u[k];
+      if (in) store(o.ptr, row * N + col, col, g);
+      __builtin_amdgcn_sched_barrier(0);   // as above
+    }
+  }
+};
+
 template <class C, int E, bool BF>
-__global__ __attribute__((amdgpu_flat_work_group_size(C::NT, C::NT), amdgpu_waves_per_eu(C::NW * C::PERCU / 4)))
+__global__ __attribute__((amdgpu_flat_work_group_size(C::NT, C::NT), amdgpu_waves_per_eu(2)))
 void tgemm_int8(MArgs a) {
   constexpr int FM = C::FM, FN = C::FN, D = C::D, U = C::U;
   __shared__ __attribute__((aligned(1024))) int8_t smem[C::kLds];
+  __shared__ __attribute__((aligned(256))) float aux[C::kAuxBytes / 4];
   const uint32_t lbase = (uint32_t)(uintptr_t)smem;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -96,10 +347,43 @@ void tgemm_int8(MArgs a) {
   };
   auto load = [&](int i, int st, int32_t s) {
     if (i < C::kALoads)
-      dma16(lbase + st * C::kStage + 1024 * (C::kALoads * wave + i), offA[i < C::kALoads ? i : 0], ab + C::KS * s);
+      dma16(__builtin_amdgcn_readfirstlane(lbase + st * C::kStage + 1024 * (C::kALoads * wave + i)),
+            offA[i < C::kALoads ? i : 0], ab + C::KS * s);
     else
-      dma16(lbase + st * C::kStage + C::kAStage + 1024 * (C::kWLoads * wave + i - C::kALoads),
+      dma16(__builtin_amdgcn_readfirstlane(lbase + st * C::kStage + C::kAStage + 1024 * (C::kWLoads * wave + i - C::kALoads)),
             offW[i >= C::kALoads ? i - C::kALoads : 0], wb + C::KS * s);
+  };
+  // the scales and biases of tile it, 64 a load: row scales, then the columns'
+  // scales, then their biases (gated: the gate's, then the up projection's)
+  auto load_aux = [&](int32_t it) {
+    int64_t m0, n0;
+    tile_at(it, m0, n0);
+#pragma unroll
+    for (int i = 0; i < C::kAuxLoads; ++i) {
+      const int x = wave + C::NW * i;
+      const float *src = a.o.rs + m0;
+      int64_t left = a.R - m0;
+      int at = 64 * x + lane;
+      uint32_t half = 0;   // elements from the gate's biases to the up projection's
+      if (x >= C::BM / 64) {
+        at = 64 * ((x - C::BM / 64) % (C::BN / 64)) + lane;
+        src = x >= C::BM / 64 + C::BN / 64 ? a.o.bias : a.o.cs;
+        left = a.Cc - n0;
+        if constexpr (E & EPI_GATED) {
+          left /= 2;
+          if (src) src += n0 / 2;
+          if (at >= C::BN / 2) {
+            at -= C::BN / 2;
+            half = (uint32_t)(a.Cc / 2);
+          }
+        } else if (src) {
+          src += n0;
+        }
+      }
+      if (x < C::kAux && src)
+        dma4(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)aux + 256 * x),
+             4 * ((uint32_t)(at < left ? at : left - 1) + half), src);
+    }
   };
   int32_t it_ld = 0, s_ld = 0;
   auto next_load = [&]() {
@@ -138,40 +422,40 @@ void tgemm_int8(MArgs a) {
   auto frag_q = [&](int st, int u, int i) { return *reinterpret_cast<const v4i *>(smem + st * C::kStage + qoff[u] + i * 16 * C::KS); };
   auto frag_p = [&](int st, int u, int j) { return *reinterpret_cast<const v4i *>(smem + st * C::kStage + poff[u] + j * 16 * C::KS); };
   wait_barrier<(D - 1) * C::kBatch>();
-#pragma unroll
-  for (int i = 0; i < FM; ++i) q[0][i] = frag_q(0, 0, i);
-#pragma unroll
-  for (int j = 0; j < FN; ++j) p[0][j] = frag_p(0, 0, j);
-
   constexpr int kStores = E & EPI_GATED ? FM * (BF || FN == 2 ? 1 : 2) : FM * (BF ? FN / 2 + FN % 2 : FN);
   static_assert(C::kWait + kStores <= 63, "vmcnt field");
   int st = 0, after = 0;
-  for (int32_t it = 0; it < ntile; ++it) {
-    for (int32_t s = 0; s < a.nk; ++s) {
-      const int st1 = st + 1 == D ? 0 : st + 1;
+  // One step: its products, the loads of step g + D into the stage that it frees,
+  // and, but for a tile's last step, the first fragments of the step after it.
+  auto step = [&](int32_t it, int32_t s, auto last) __attribute__((always_inline)) {
+    constexpr bool kLast = decltype(last)::value;
+    const int st1 = st + 1 == D ? 0 : st + 1;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int cur = u & 1, nxt = U == 1 ? 0 : cur ^ 1;
-        constexpr int kBar = C::FM * 3 / 8;   // the slot that the barrier comes before
-        const int first = u == U - 1 ? kBar : 0, slots = FM - first;
-        v4i qn[FM], pn[FN];
-        // chunks of the last step past the contraction: A's count as zeros
-        if (s == a.nk - 1 && a.tail != C::CH && 4 * u + (lane >> 4) >= a.tail) {
+    for (int u = 0; u < U; ++u) {
+      const int cur = u & 1, nxt = U == 1 ? 0 : cur ^ 1;
+      constexpr int kBar = C::FM * 3 / 8;   // the slot that the barrier comes before
+      const bool reads = u + 1 < U || !kLast;
+      const int first = u == U - 1 ? kBar : 0, slots = FM - first;
+      v4i qn[FM], pn[FN];
+      // chunks past the contraction: A's count as zeros
+      if (kLast && a.tail != C::CH && 4 * u + (lane >> 4) >= a.tail) {
 #pragma unroll
-          for (int i = 0; i < FM; ++i) q[cur][i] = v4i{0, 0, 0, 0};
+        for (int i = 0; i < FM; ++i) q[cur][i] = v4i{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if (u == U - 1 && i == kBar) {
+          if (after)
+            wait_barrier<C::kWait + kStores>();
+          else
+            wait_barrier<C::kWait>();
+          after = 0;
+          if (s == 0) load_aux(it);   // every wave has written the tile before
         }
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          if (u == U - 1 && i == kBar) {
-            if (after)
-              wait_barrier<C::kWait + kStores>();
-            else
-              wait_barrier<C::kWait>();
-            after = 0;
-          }
-          if (i >= first) {
-            const int k = i - first, sn = u + 1 < U ? st : st1, un = u + 1 < U ? u + 1 : 0;
-            // fragments of the next substep, the columns' first
+        if (i >= first) {
+          const int k = i - first, sn = u + 1 < U ? st : st1, un = u + 1 < U ? u + 1 : 0;
+          // fragments of the next substep, the columns' first
+          if (reads) {
 #pragma unroll
             for (int x = k * (FM + FN) / slots; x < (k + 1) * (FM + FN) / slots; ++x) {
               if (x < FN)
@@ -179,44 +463,52 @@ void tgemm_int8(MArgs a) {
               else
                 qn[x >= FN ? x - FN : 0] = frag_q(sn, un, x - FN);
             }
-            if (u == U - 1) {
-#pragma unroll
-              for (int x = k * C::kBatch / slots; x < (k + 1) * C::kBatch / slots; ++x) load(x, st, s_ld);
-            }
           }
+          if (u == U - 1) {
 #pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(p[cur][j], q[cur][i], acc[i][j], 0, 0, 0);
-          __builtin_amdgcn_sched_barrier(0);
+            for (int x = k * C::kBatch / slots; x < (k + 1) * C::kBatch / slots; ++x) load(x, st, s_ld);
+          }
         }
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(p[cur][j], q[cur][i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (reads) {
 #pragma unroll
         for (int i = 0; i < FM; ++i) q[nxt][i] = qn[i];
 #pragma unroll
         for (int j = 0; j < FN; ++j) p[nxt][j] = pn[j];
       }
-      next_load();
-      st = st1;
     }
+    next_load();
+    st = st1;
+  };
+  for (int32_t it = 0; it < ntile; ++it) {
+    // a tile's first fragments (its first stage was published with the last one
+    // of the tile before, whose end needs the registers)
+#pragma unroll
+    for (int i = 0; i < FM; ++i) q[0][i] = frag_q(st, 0, i);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) p[0][j] = frag_p(st, 0, j);
+    for (int32_t s = 0; s + 1 < a.nk; ++s) step(it, s, Flag<false>());
+    step(it, a.nk - 1, Flag<true>());
     int64_t m0, n0;
     tile_at(it, m0, n0);
-    const int64_t r0 = m0 + wm * C::TM, c0 = n0 + wn * C::TN;
-    float rs[FM];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int64_t row = r0 + (lane >> 2) + 16 * i;
-      rs[i] = a.o.rs[row < a.R ? row : a.R - 1];
-    }
+    // the scales have landed once D - 2 whole batches were waited for after them
+    if (a.nk < D) wait_barrier<0>();
     const bool inside = m0 + C::BM <= a.R && n0 + C::BN <= a.Cc;
+    const int64_t r0 = m0 + wm * C::TM, c0 = n0 + wn * C::TN;
     if constexpr (E & EPI_GATED) {
       if (inside)
-        gated_tile<E, BF, false>(a.o, a.R, a.Cc / 2, acc, r0, c0 / 2, lane, rs);
+        GatedOut<C, E, BF, false>{a.o, aux, a.R, a.Cc / 2, r0, c0 / 2, wm * C::TM, wn * C::TN / 2, lane}.run(acc);
       else
-        gated_tile<E, BF, true>(a.o, a.R, a.Cc / 2, acc, r0, c0 / 2, lane, rs);
+        GatedOut<C, E, BF, true>{a.o, aux, a.R, a.Cc / 2, r0, c0 / 2, wm * C::TM, wn * C::TN / 2, lane}.run(acc);
     } else {
       if (inside)
-        epi_tile<E, BF, false>(a.o, a.R, a.Cc, acc, r0, c0, lane, rs);
+        PlainOut<C, E, BF, false>{a.o, aux, a.R, a.Cc, r0, c0, wm * C::TM, wn * C::TN, lane}.run(acc);
       else
-        epi_tile<E, BF, true>(a.o, a.R, a.Cc, acc, r0, c0, lane, rs);
+        PlainOut<C, E, BF, true>{a.o, aux, a.R, a.Cc, r0, c0, wm * C::TM, wn * C::TN, lane}.run(acc);
     }
     after = inside;
 #pragma unroll
@@ -427,6 +719,7 @@ bool mul_ok(int64_t a, int64_t b, int64_t *out) {
   *out = a * b;
   return true;
 }
+constexpr int64_t kMaxCols = (int64_t)1 << 29;   // a tile's loads of biases reach 4 N bytes in 32 bits
 int check_sizes(int64_t M, int64_t N, int64_t K) {
   int64_t t;
   if (M < 1 || N < 1 || K < 1) return TGEMM_ERR_DIM;
@@ -434,12 +727,13 @@ int check_sizes(int64_t M, int64_t N, int64_t K) {
   if (!mul_ok(M, K, &t) || !mul_ok(t, 8, &t) || !mul_ok(N, K, &t) || !mul_ok(t, 8, &t) || !mul_ok(M, N, &t) ||
       !mul_ok(t, 8, &t))
     return TGEMM_ERR_DIM;
-  if (M > INT64_MAX / 2 / 64 || N > INT32_MAX || ceil_div(M, 16) * ceil_div(2 * N, 16) > INT32_MAX) return TGEMM_ERR_DIM;
+  if (N > kMaxCols || ceil_div(M, 16) * ceil_div(2 * N, 16) > INT32_MAX) return TGEMM_ERR_DIM;
   return TGEMM_OK;
 }
 
 typedef mm::Cfg<256, 128, 4, 2, 128, 3, 1> Large;
 typedef mm::Cfg<128, 128, 2, 2, 128, 2, 2> Mid;
+typedef mm::Cfg<128, 128, 2, 4, 128, 4, 1> Deep;
 typedef mm::Cfg<64, 128, 2, 2, 128, 3, 2> Small;
 typedef mm::Cfg<64, 64, 2, 2, 128, 4, 2> Tiny;
 
@@ -449,7 +743,7 @@ int launch_mm(MArgs a, const Machine &mc, hipStream_t stream) {
   a.tiles_c = (int32_t)ceil_div(a.Cc, C::BN);
   a.tiles = a.tiles_r * a.tiles_c;
   a.xcds = mc.xcds;
-  a.band_cols = a.tiles_c < 4 ? a.tiles_c : 4;
+  a.band_cols = a.tiles_c < 8 ? a.tiles_c : 8;
   a.nk = (int32_t)ceil_div(a.K, C::KS);
   a.tail = (int32_t)((a.K - (int64_t)(a.nk - 1) * C::KS) / 16);
   int64_t grid = (int64_t)mc.cus * C::PERCU;
@@ -461,15 +755,17 @@ int launch_mm(MArgs a, const Machine &mc, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
 }
 template <class C>
-int64_t rounds(int64_t R, int64_t Cc, const Machine &mc) {
-  return ceil_div(ceil_div(R, C::BM) * ceil_div(Cc, C::BN), (int64_t)mc.cus * C::PERCU);
+int64_t tiles_of(const MArgs &a) {
+  return ceil_div(a.R, C::BM) * ceil_div(a.Cc, C::BN);
 }
 template <int E>
 int pick_mm(const MArgs &a, const Machine &mc, hipStream_t stream) {
-  if (ceil_div(a.R, 128) * ceil_div(a.Cc, 128) <= mc.cus / 2) return launch_mm<Tiny, E>(a, mc, stream);
-  if (ceil_div(a.R, 128) * ceil_div(a.Cc, 128) <= mc.cus) return launch_mm<Small, E>(a, mc, stream);
-  if (ceil_div(a.R, 256) * ceil_div(a.Cc, 128) < mc.cus) return launch_mm<Mid, E>(a, mc, stream);
-  return launch_mm<Large, E>(a, mc, stream);
+  const int64_t cus = mc.cus, large = tiles_of<Large>(a);
+  if (tiles_of<Tiny>(a) <= cus) return launch_mm<Tiny, E>(a, mc, stream);
+  if (tiles_of<Small>(a) <= cus) return launch_mm<Small, E>(a, mc, stream);
+  if (tiles_of<Deep>(a) <= cus) return launch_mm<Deep, E>(a, mc, stream);
+  if (large <= cus || 4 * large >= 3 * round_up(large, cus)) return launch_mm<Large, E>(a, mc, stream);
+  return launch_mm<Mid, E>(a, mc, stream);
 }
 template <int FLAG>
 int pick_mm_act(const MArgs &a, const Machine &mc, hipStream_t stream) {

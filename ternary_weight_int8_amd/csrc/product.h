@@ -271,25 +271,7 @@ __device__ __forceinline__ void epi_run(const Out &o, int64_t Cc, const v4i (&ac
 #pragma unroll
     for (int jj = 0; jj < N; ++jj)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int32_t x = __builtin_amdgcn_ds_bpermute(src, v[jj][e]);
-        y[jj][e] = E & EPI_COLS ? __fmul_rn((float)x, rs) : scaled(x, rs, o.cscal);
-      }
-  }
-  if ((E & EPI_COLS) && o.cs) {
-#pragma unroll
-    for (int jj = 0; jj < N; ++jj) {
-      const int64_t col = col_of(jj);
-      if (!GUARD || col + 3 < Cc) {
-        const v4f_u b = *reinterpret_cast<const v4f_u *>(o.cs + col);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[jj][e] *= b[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < Cc) y[jj][e] *= o.cs[col + e];
-      }
-    }
+      for (int e = 0; e < 4; ++e) y[jj][e] = scaled(__builtin_amdgcn_ds_bpermute(src, v[jj][e]), rs, o.cscal);
   }
   if (o.bias) {
 #pragma unroll
@@ -307,7 +289,7 @@ __device__ __forceinline__ void epi_run(const Out &o, int64_t Cc, const v4i (&ac
     }
   }
   if (o.z) store(o.z);
-  if ((E & kEpiAct) != EPI_POLY || o.act != TGEMM_ACT_NONE) {
+  if (E != EPI_POLY || o.act != TGEMM_ACT_NONE) {
 #pragma unroll
     for (int jj = 0; jj < N; ++jj)
 #pragma unroll
@@ -385,111 +367,6 @@ __device__ __forceinline__ void gated_put(const Out &o, int64_t No, int64_t row,
       store1(o.z, o.kind, (2 * row + 1) * No + c, u);
     }
     store1(o.ptr, o.kind, row * No + c, epi_act<E>(g, o.act) * u);
-  }
-}
-
-// fragments F0 .. F0 + N - 1 (N 2 or 4) of a fragment row: lane groups and
-// registers are exchanged (permlane swaps) until group p of 16 lanes holds 4 N
-// neighbouring columns, and ds_bpermute then gives four neighbouring lanes a
-// row: a lane has 2 N neighbouring outputs, and a row's four lanes 8 N.
-template <int E, bool BF, bool GUARD, int F0, int N, int FN>
-__device__ __forceinline__ void gated_run(const Out &o, int64_t No, const v4i (&acc)[FN], int64_t row, bool in, int64_t c0,
-                                          int lane, float rs) {
-#pragma clang fp contract(off)   // every kernel rounds alike
-  constexpr int kKind = BF ? OUT_BF16 : OUT_F32, kOut = 2 * N;
-  static_assert(N == 2 || N == 4, "pairs or fours of fragments");
-  asm volatile("" : "+v"(lane));   // as in epi_run
-  const int p = lane & 3, src = 4 * ((lane >> 2) + 16 * p);
-  const int64_t col = c0 + 8 * F0 + kOut * p;
-  const bool whole = !GUARD || col + kOut <= No;
-  float g[kOut], u[kOut];
-  {
-    v4i v[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = acc[F0 + j];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (N == 4) {
-        const auto a = __builtin_amdgcn_permlane32_swap(v[0][e], v[2][e], false, false);
-        const auto b = __builtin_amdgcn_permlane32_swap(v[1][e], v[3][e], false, false);
-        const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-        const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-        v[0][e] = c[0];
-        v[1][e] = c[1];
-        v[2][e] = d[0];
-        v[3][e] = d[1];
-      } else {
-        const auto a = __builtin_amdgcn_permlane32_swap(v[0][e], v[1][e], false, false);
-        const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[1], false, false);
-        v[0][e] = b[0];
-        v[1][e] = b[1];
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        g[2 * j + e] = scaled(__builtin_amdgcn_ds_bpermute(src, v[j][2 * e]), rs, o.cscal);
-        u[2 * j + e] = scaled(__builtin_amdgcn_ds_bpermute(src, v[j][2 * e + 1]), rs, o.cscal2);
-      }
-  }
-  auto add = [&](float (&y)[kOut], const float *b) {
-#pragma unroll
-    for (int k = 0; k < kOut; k += 4) {
-      if (whole) {
-        const v4f_u x = *reinterpret_cast<const v4f_u *>(b + col + k);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[k + e] += x[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + k + e < No) y[k + e] += b[col + k + e];
-      }
-    }
-  };
-  auto store = [&](void *base, int64_t at, const float (&y)[kOut]) {
-    if (!in) return;
-    if (whole) {
-      if constexpr (BF && kOut == 8) {
-        *reinterpret_cast<v4u_u *>(static_cast<uint16_t *>(base) + at) =
-            v4u_u{bf16_pack(y[0], y[1]), bf16_pack(y[2], y[3]), bf16_pack(y[4], y[5]), bf16_pack(y[6], y[7])};
-      } else {
-#pragma unroll
-        for (int k = 0; k < kOut; k += 4) store4(base, kKind, at + k, {y[k], y[k + 1], y[k + 2], y[k + 3]});
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kOut; ++k)
-        if (col + k < No) store1(base, kKind, at + k, y[k]);
-    }
-  };
-  if (o.bias) {
-    add(g, o.bias);
-    add(u, o.bias + No);
-  }
-  if (o.z) {
-    store(o.z, 2 * row * No + col, g);
-    store(o.z, (2 * row + 1) * No + col, u);
-  }
-  if ((E & kEpiAct) != EPI_POLY || o.act != TGEMM_ACT_NONE) {
-#pragma unroll
-    for (int k = 0; k < kOut; ++k) g[k] = epi_act<E>(g[k], o.act);
-  }
-#pragma unroll
-  for (int k = 0; k < kOut; ++k) g[k] *= u[k];
-  store(o.ptr, row * No + col, g);
-  __builtin_amdgcn_sched_barrier(0);   // as in epi_run
-}
-
-// a wave's FM x FN fragments; c0 is the first output column
-template <int E, bool BF, bool GUARD, int FM, int FN>
-__device__ __forceinline__ void gated_tile(const Out &o, int64_t R, int64_t No, const v4i (&acc)[FM][FN], int64_t r0,
-                                           int64_t c0, int lane, const float (&rs)[FM]) {
-  static_assert(FN == 2 || FN == 4, "fragments");
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t row = r0 + (lane >> 2) + 16 * i;
-    gated_run<E, BF, GUARD, 0, FN, FN>(o, No, acc[i], row, !GUARD || row < R, c0, lane, rs[i]);
   }
 }
 
