@@ -195,98 +195,109 @@ struct PlainOut {
 //   aux: BM row scales, BN of nothing, BN / 2 biases of the gate, BN / 2 of the up projection
 template <class C, int E, bool BF, bool GUARD>
 struct GatedOut {
-  static constexpr int FM = C::FM, FN = C::FN, kKind = BF ? OUT_BF16 : OUT_F32, kOut = 2 * FN;
-  static_assert(FN == 2 || FN == 4, "pairs or fours of fragments");
+  static constexpr int FM = C::FM, FN = C::FN, kKind = BF ? OUT_BF16 : OUT_F32;
+  static_assert(FN % 2 == 0, "pairs of fragments");
   const Out &o;
   const float *aux;
   int64_t R, N, r0, c0;    // N, c0 and cl count outputs
   int rl, cl;
   int lane;
 
-  __device__ __forceinline__ void store(void *base, int64_t at, int64_t col, const float (&y)[kOut]) const {
-    if (!GUARD || col + kOut <= N) {
-      if constexpr (BF && kOut == 8) {
+  template <int OUT>
+  __device__ __forceinline__ void store(void *base, int64_t at, int64_t col, const float (&y)[OUT]) const {
+    if (!GUARD || col + OUT <= N) {
+      if constexpr (BF && OUT == 8) {
         *reinterpret_cast<v4u_u *>(static_cast<uint16_t *>(base) + at) =
             v4u_u{bf16_pack(y[0], y[1]), bf16_pack(y[2], y[3]), bf16_pack(y[4], y[5]), bf16_pack(y[6], y[7])};
       } else {
 #pragma unroll
-        for (int k = 0; k < kOut; k += 4) store4(base, kKind, at + k, {y[k], y[k + 1], y[k + 2], y[k + 3]});
+        for (int k = 0; k < OUT; k += 4) store4(base, kKind, at + k, {y[k], y[k + 1], y[k + 2], y[k + 3]});
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < kOut; ++k)
+      for (int k = 0; k < OUT; ++k)
         if (col + k < N) store1(base, kKind, at + k, y[k]);
     }
   }
-  __device__ __forceinline__ void run(const v4i (&acc)[FM][FN]) const {
+  // fragments F0 .. F0 + F - 1 (F 2 or 4) of fragment row i
+  template <int F0, int F>
+  __device__ __forceinline__ void part(const v4i (&acc)[FM][FN], int i) const {
 #pragma clang fp contract(off)   // every kernel rounds alike
-    const int p = lane & 3, src = 4 * ((lane >> 2) + 16 * p);
-    const float *bias = aux + C::BM + C::BN + cl + kOut * p;
-    const int64_t col = c0 + kOut * p;
+    constexpr int kOut = 2 * F;
+    const int p = lane & 3, src = 4 * ((lane >> 2) + 16 * p), at = 8 * F0 + kOut * p;
+    const int64_t row = r0 + (lane >> 2) + 16 * i, col = c0 + at;
+    const float rs = aux[rl + (lane >> 2) + 16 * i];
+    float g[kOut], u[kOut];
+    {
+      v4i v[F];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int64_t row = r0 + (lane >> 2) + 16 * i;
-      const float rs = aux[rl + (lane >> 2) + 16 * i];
-      float g[kOut], u[kOut];
-      {
-        v4i v[FN];
+      for (int j = 0; j < F; ++j) v[j] = acc[i][F0 + j];
 #pragma unroll
-        for (int j = 0; j < FN; ++j) v[j] = acc[i][j];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (FN == 4) {
-            const auto a = __builtin_amdgcn_permlane32_swap(v[0][e], v[2][e], false, false);
-            const auto b = __builtin_amdgcn_permlane32_swap(v[1][e], v[3][e], false, false);
-            const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-            const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-            v[0][e] = c[0];
-            v[1][e] = c[1];
-            v[2][e] = d[0];
-            v[3][e] = d[1];
-          } else {
-            const auto a = __builtin_amdgcn_permlane32_swap(v[0][e], v[1][e], false, false);
-            const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[1], false, false);
-            v[0][e] = b[0];
-            v[1][e] = b[1];
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            g[2 * j + e] = scaled(__builtin_amdgcn_ds_bpermute(src, v[j][2 * e]), rs, o.cscal);
-            u[2 * j + e] = scaled(__builtin_amdgcn_ds_bpermute(src, v[j][2 * e + 1]), rs, o.cscal2);
-          }
-      }
-      if (o.bias) {
-#pragma unroll
-        for (int k = 0; k < kOut; k += 4) {
-          const float4 a = *reinterpret_cast<const float4 *>(bias + k), b = *reinterpret_cast<const float4 *>(bias + C::BN / 2 + k);
-          g[k] += a.x;
-          g[k + 1] += a.y;
-          g[k + 2] += a.z;
-          g[k + 3] += a.w;
-          u[k] += b.x;
-          u[k + 1] += b.y;
-          u[k + 2] += b.z;
-          u[k + 3] += b.w;
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (F == 4) {
+          const auto a = __builtin_amdgcn_permlane32_swap(v[0][e], v[2][e], false, false);
+          const auto b = __builtin_amdgcn_permlane32_swap(v[1][e], v[3][e], false, false);
+          const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+          const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+          v[0][e] = c[0];
+          v[1][e] = c[1];
+          v[2][e] = d[0];
+          v[3][e] = d[1];
+        } else {
+          const auto a = __builtin_amdgcn_permlane32_swap(v[0][e], v[1][e], false, false);
+          const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[1], false, false);
+          v[0][e] = b[0];
+          v[1][e] = b[1];
         }
       }
-      const bool in = !GUARD || row < R;
-      if (o.z && in) {
-        store(o.z, 2 * row * N + col, col, g);
-        store(o.z, (2 * row + 1) * N + col, col, u);
-      }
-      if ((E & kEpiAct) != EPI_POLY || o.act != TGEMM_ACT_NONE) {
 #pragma unroll
-        for (int k = 0; k < kOut; ++k) g[k] = epi_act<E>(g[k], o.act);
-      }
+      for (int j = 0; j < F; ++j)
 #pragma unroll
-      for (int k = 0; k < kOut; ++k) g[k] *= u[k];
-      if (in) store(o.ptr, row * N + col, col, g);
-      __builtin_amdgcn_sched_barrier(0);   // as above
+        for (int e = 0; e < 2; ++e) {
+          g[2 * j + e] = scaled(__builtin_amdgcn_ds_bpermute(src, v[j][2 * e]), rs, o.cscal);
+          u[2 * j + e] = scaled(__builtin_amdgcn_ds_bpermute(src, v[j][2 * e + 1]), rs, o.cscal2);
+        }
     }
+    if (o.bias) {
+      const float *bias = aux + C::BM + C::BN + cl + at;
+#pragma unroll
+      for (int k = 0; k < kOut; k += 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(bias + k), b = *reinterpret_cast<const float4 *>(bias + C::BN / 2 + k);
+        g[k] += a.x;
+        g[k + 1] += a.y;
+        g[k + 2] += a.z;
+        g[k + 3] += a.w;
+        u[k] += b.x;
+        u[k + 1] += b.y;
+        u[k + 2] += b.z;
+        u[k + 3] += b.w;
+      }
+    }
+    const bool in = !GUARD || row < R;
+    if (o.z && in) {
+      store<kOut>(o.z, 2 * row * N + col, col, g);
+      store<kOut>(o.z, (2 * row + 1) * N + col, col, u);
+    }
+    if ((E & kEpiAct) != EPI_POLY || o.act != TGEMM_ACT_NONE) {
+#pragma unroll
+      for (int k = 0; k < kOut; ++k) g[k] = epi_act<E>(g[k], o.act);
+    }
+#pragma unroll
+    for (int k = 0; k < kOut; ++k) g[k] *= u[k];
+    if (in) store<kOut>(o.ptr, row * N + col, col, g);
+    __builtin_amdgcn_sched_barrier(0);   // as above
   }
+  template <int F0>
+  __device__ __forceinline__ void row_out(const v4i (&acc)[FM][FN], int i) const {
+    constexpr int F = FN - F0 >= 4 ? 4 : 2;
+    part<F0, F>(acc, i);
+    if constexpr (F0 + F < FN) row_out<F0 + F>(acc, i);
+  }
+  __device__ __forceinline__ void run(const v4i (&acc)[FM][FN]) const {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) row_out<0>(acc, i);
+  }
+  static constexpr int kStores = FM * (BF ? (FN + 2) / 4 : FN / 2);   // of a whole tile, without Z's
 };
 
 template <class C, int E, bool BF>
@@ -422,7 +433,7 @@ void tgemm_int8(MArgs a) {
   auto frag_q = [&](int st, int u, int i) { return *reinterpret_cast<const v4i *>(smem + st * C::kStage + qoff[u] + i * 16 * C::KS); };
   auto frag_p = [&](int st, int u, int j) { return *reinterpret_cast<const v4i *>(smem + st * C::kStage + poff[u] + j * 16 * C::KS); };
   wait_barrier<(D - 1) * C::kBatch>();
-  constexpr int kStores = E & EPI_GATED ? FM * (BF || FN == 2 ? 1 : 2) : FM * (BF ? FN / 2 + FN % 2 : FN);
+  constexpr int kStores = E & EPI_GATED ? GatedOut<C, E, BF, false>::kStores : FM * (BF ? FN / 2 : FN);
   static_assert(C::kWait + kStores <= 63, "vmcnt field");
   int st = 0, after = 0;
   // One step: its products, the loads of step g + D into the stage that it frees,
@@ -433,10 +444,8 @@ void tgemm_int8(MArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int cur = u & 1, nxt = U == 1 ? 0 : cur ^ 1;
-      constexpr int kBar = C::FM * 3 / 8;   // the slot that the barrier comes before
-      const bool reads = u + 1 < U || !kLast;
-      const int first = u == U - 1 ? kBar : 0, slots = FM - first;
-      v4i qn[FM], pn[FN];
+          const bool reads = u + 1 < U || !kLast;
+            v4i qn[FM], pn[FN];
       // chunks past the contraction: A's count as zeros
       if (kLast && a.tail != C::CH && 4 * u + (lane >> 4) >= a.tail) {
 #pragma unroll
@@ -444,7 +453,7 @@ void tgemm_int8(MArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        if (u == U - 1 && i == kBar) {
+        if (u == U - 1 && i == 0) {
           if (after)
             wait_barrier<C::kWait + kStores>();
           else
@@ -452,22 +461,20 @@ void tgemm_int8(MArgs a) {
           after = 0;
           if (s == 0) load_aux(it);   // every wave has written the tile before
         }
-        if (i >= first) {
-          const int k = i - first, sn = u + 1 < U ? st : st1, un = u + 1 < U ? u + 1 : 0;
-          // fragments of the next substep, the columns' first
-          if (reads) {
+        const int sn = u + 1 < U ? st : st1, un = u + 1 < U ? u + 1 : 0;
+        // fragments of the next substep, the columns' first
+        if (reads) {
 #pragma unroll
-            for (int x = k * (FM + FN) / slots; x < (k + 1) * (FM + FN) / slots; ++x) {
-              if (x < FN)
-                pn[x < FN ? x : 0] = frag_p(sn, un, x);
-              else
-                qn[x >= FN ? x - FN : 0] = frag_q(sn, un, x - FN);
-            }
+          for (int x = i * (FM + FN) / FM; x < (i + 1) * (FM + FN) / FM; ++x) {
+            if (x < FN)
+              pn[x < FN ? x : 0] = frag_p(sn, un, x);
+            else
+              qn[x >= FN ? x - FN : 0] = frag_q(sn, un, x - FN);
           }
-          if (u == U - 1) {
+        }
+        if (u == U - 1) {
 #pragma unroll
-            for (int x = k * C::kBatch / slots; x < (k + 1) * C::kBatch / slots; ++x) load(x, st, s_ld);
-          }
+          for (int x = i * C::kBatch / FM; x < (i + 1) * C::kBatch / FM; ++x) load(x, st, s_ld);
         }
 #pragma unroll
         for (int j = 0; j < FN; ++j)
@@ -731,11 +738,12 @@ int check_sizes(int64_t M, int64_t N, int64_t K) {
   return TGEMM_OK;
 }
 
-typedef mm::Cfg<256, 128, 4, 2, 128, 3, 1> Large;
-typedef mm::Cfg<128, 128, 2, 2, 128, 2, 2> Mid;
-typedef mm::Cfg<128, 128, 2, 4, 128, 4, 1> Deep;
-typedef mm::Cfg<64, 128, 2, 2, 128, 3, 2> Small;
-typedef mm::Cfg<64, 64, 2, 2, 128, 4, 2> Tiny;
+typedef mm::Cfg<256, 192, 4, 2, 128, 2, 1> T256x192;
+typedef mm::Cfg<256, 128, 4, 2, 128, 3, 1> T256x128;
+typedef mm::Cfg<128, 192, 4, 2, 128, 3, 1> T128x192;
+typedef mm::Cfg<128, 128, 2, 4, 128, 4, 1> T128x128;
+typedef mm::Cfg<64, 128, 2, 2, 128, 3, 2> T64x128;
+typedef mm::Cfg<64, 64, 2, 2, 128, 4, 2> T64x64;
 
 template <class C, int E>
 int launch_mm(MArgs a, const Machine &mc, hipStream_t stream) {
@@ -754,18 +762,43 @@ int launch_mm(MArgs a, const Machine &mc, hipStream_t stream) {
     hipLaunchKernelGGL((tgemm_int8<C, E, false>), dim3((unsigned)grid), dim3(C::NT), 0, stream, a);
   return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
 }
+// The tile with the least estimated time: rounds of tiles over the CUs, each of
+// so many us a step and at its end, as measured with every CU at work (fitted to
+// 31 sizes of 65 to 16384 rows; the choice is the fastest of these six or within
+// 2% of it on 27 of them, and 1.7% slower in the mean).  A last round that leaves
+// CUs idle has faster steps; of the two kernels with two workgroups a CU, a last
+// round of one a CU has its own figures.
+struct TileTime {
+  double step, end, step1, end1;
+};
 template <class C>
-int64_t tiles_of(const MArgs &a) {
-  return ceil_div(a.R, C::BM) * ceil_div(a.Cc, C::BN);
+double time_of(const MArgs &a, const Machine &mc, const TileTime &t) {
+  const int64_t tiles = ceil_div(a.R, C::BM) * ceil_div(a.Cc, C::BN), slots = (int64_t)mc.cus * C::PERCU;
+  const double steps = (double)ceil_div(a.K, C::KS);
+  const int64_t rem = tiles % slots;
+  double us = (double)(tiles / slots) * (t.step * steps + t.end);
+  if (rem && C::PERCU == 2 && rem <= mc.cus)
+    us += t.step1 * steps + t.end1;
+  else if (rem)
+    us += t.step * (0.75 + 0.25 * (double)rem / (double)slots) * steps + t.end;
+  return us;
 }
 template <int E>
 int pick_mm(const MArgs &a, const Machine &mc, hipStream_t stream) {
-  const int64_t cus = mc.cus, large = tiles_of<Large>(a);
-  if (tiles_of<Tiny>(a) <= cus) return launch_mm<Tiny, E>(a, mc, stream);
-  if (tiles_of<Small>(a) <= cus) return launch_mm<Small, E>(a, mc, stream);
-  if (tiles_of<Deep>(a) <= cus) return launch_mm<Deep, E>(a, mc, stream);
-  if (large <= cus || 4 * large >= 3 * round_up(large, cus)) return launch_mm<Large, E>(a, mc, stream);
-  return launch_mm<Mid, E>(a, mc, stream);
+  const double us[] = {time_of<T256x192>(a, mc, {1.0, 5.4, 0, 0}), time_of<T256x128>(a, mc, {0.82, 3.3, 0, 0}),
+                       time_of<T128x192>(a, mc, {0.6, 2.6, 0, 0}), time_of<T128x128>(a, mc, {0.47, 2.0, 0, 0}),
+                       time_of<T64x128>(a, mc, {0.58, 1.8, 0.34, 1.0}), time_of<T64x64>(a, mc, {0.37, 1.0, 0.2, 0.6})};
+  int best = 0;
+  for (int i = 1; i < 6; ++i)
+    if (us[i] < us[best]) best = i;
+  switch (best) {
+    case 0: return launch_mm<T256x192, E>(a, mc, stream);
+    case 1: return launch_mm<T256x128, E>(a, mc, stream);
+    case 2: return launch_mm<T128x192, E>(a, mc, stream);
+    case 3: return launch_mm<T128x128, E>(a, mc, stream);
+    case 4: return launch_mm<T64x128, E>(a, mc, stream);
+    default: return launch_mm<T64x64, E>(a, mc, stream);
+  }
 }
 template <int FLAG>
 int pick_mm_act(const MArgs &a, const Machine &mc, hipStream_t stream) {
