@@ -402,7 +402,7 @@ int ternary_layernorm_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
  * this call on dZ's int8 rows and the transposed weights, quantized row by row
  * like the weights; dW is ternary_gemm_s8_dw_scaled on both operands' columns.
  * Workspace: where K is not a multiple of 16 or an operand's base not 16-byte
- * aligned, more than 64 rows need it (the operand is copied into aligned rows).
+ * aligned, more than 64 rows need it (operands are copied into aligned rows).
  * The query takes the smallest alignment of A and W, in bytes.
  */
 int ternary_gemm_s8s8_epilogue(const int8_t *A, const int8_t *W, const float *a_row_scale, const float *w_col_scale,
@@ -425,9 +425,9 @@ int ternary_gemm_s8s8_workspace(int64_t M, int64_t N, int64_t K, int64_t align, 
  *   bias     float [2N], or NULL
  *   Y        [M][N] of out_kind
  *   Z        [M][2N] of out_kind, (g | u) for ternary_gated_backward, or NULL
- * Workspace: more than 64 rows need one (the weights' codes are decoded into it,
- * 2 N K bytes), and so do fewer where K is not a multiple of 64 or A or Wpacked
- * not 16-byte aligned.  The query takes their smallest alignment, in bytes.
+ * Workspace: more than 128 to 192 rows need one (the weights' codes are decoded
+ * into it, 2 N K bytes), and so do fewer where K is not a multiple of 64 or A or
+ * Wpacked not 16-byte aligned.  The query takes their smallest alignment, in bytes.
  */
 int ternary_gemm_s8_gated(const int8_t *A, const uint8_t *Wpacked, const float *a_row_scale, float gate_scale,
                           float up_scale, const float *bias, int act, void *Y, void *Z, int out_kind, int64_t M,

@@ -3,8 +3,8 @@
 //   ternary_gemm_s8s8_epilogue  int8 rows times int8 weights, a scale a row and
 //                               a scale a column, bias, activation, residual
 //   ternary_gemm_s8_gated       int8 rows times the ternary weights of a gate and
-//                               of an up projection, act(g) u (64 rows and less
-//                               are multiplied in ternary_gemm.hip)
+//                               of an up projection, act(g) u (few rows are
+//                               multiplied in ternary_gemm.hip)
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -433,9 +433,12 @@ void tgemm_int8(MArgs a) {
   auto frag_q = [&](int st, int u, int i) { return *reinterpret_cast<const v4i *>(smem + st * C::kStage + qoff[u] + i * 16 * C::KS); };
   auto frag_p = [&](int st, int u, int j) { return *reinterpret_cast<const v4i *>(smem + st * C::kStage + poff[u] + j * 16 * C::KS); };
   wait_barrier<(D - 1) * C::kBatch>();
+  // stores of a whole tile: without Z, and with it.  They are younger than the
+  // loads that the next tile's first barrier waits for, which therefore counts them.
   constexpr int kStores = E & EPI_GATED ? GatedOut<C, E, BF, false>::kStores : FM * (BF ? FN / 2 : FN);
-  static_assert(C::kWait + kStores <= 63, "vmcnt field");
-  int st = 0, after = 0;
+  constexpr int kStoresZ = (E & EPI_GATED ? 3 : 2) * kStores;
+  static_assert(C::kWait + kStoresZ <= 63, "vmcnt field");
+  int st = 0, after = 0;   // after: 1 or 2, a tile without or with Z was stored right before this step
   // One step: its products, the loads of step g + D into the stage that it frees,
   // and, but for a tile's last step, the first fragments of the step after it.
   auto step = [&](int32_t it, int32_t s, auto last) __attribute__((always_inline)) {
@@ -454,7 +457,9 @@ void tgemm_int8(MArgs a) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         if (u == U - 1 && i == 0) {
-          if (after)
+          if (after == 2)
+            wait_barrier<C::kWait + kStoresZ>();
+          else if (after)
             wait_barrier<C::kWait + kStores>();
           else
             wait_barrier<C::kWait>();
@@ -517,7 +522,7 @@ void tgemm_int8(MArgs a) {
       else
         PlainOut<C, E, BF, true>{a.o, aux, a.R, a.Cc, r0, c0, wm * C::TM, wn * C::TN, lane}.run(acc);
     }
-    after = inside;
+    after = !inside ? 0 : a.o.z ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -529,17 +534,15 @@ void tgemm_int8(MArgs a) {
 
 // ---------------------------------------------------------------------------
 // Few rows (s8s8): the weights are nearly all of the bytes, and a workgroup of 8
-// waves owns 16 NB columns and 16 MF rows.  Its waves split the contraction into
-// super-steps of 256 (wave w takes w, w + 8, ...), operands straight into
+// or 16 waves owns 16 NB columns and 16 MF rows.  Its waves split the contraction
+// into super-steps of 256 (wave w takes w, w + 8, ... or w, w + 16, ...), operands straight into
 // registers a super-step ahead, and their sums meet in LDS, in wave order.
 // Lane l loads 16 bytes of row l % 16 at 64 q + 16 (l / 16), so that load q
 // takes 64 bytes of 16 rows, and q = 0 .. 3 are the four MFMA steps of the
 // super-step.  Any contraction and any alignment: loads are byte-aligned
 // vectors, and the last, partial super-step reads the bytes inside one by one.
 // ---------------------------------------------------------------------------
-namespace few {
-constexpr int kWaves = 8, kNT = 64 * kWaves, kStep = 256;
-}
+constexpr int kFewStep = 256;
 typedef int32_t v4i_u __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32_u __attribute__((aligned(1)));
 
@@ -560,10 +563,10 @@ __device__ __forceinline__ v4i load_part(const int8_t *p, int64_t n) {
   return v4i{(int32_t)w[0], (int32_t)w[1], (int32_t)w[2], (int32_t)w[3]};
 }
 
-template <int MF, int NB, int E>
-__global__ __attribute__((amdgpu_flat_work_group_size(few::kNT, few::kNT), amdgpu_waves_per_eu(2)))
+template <int MF, int NB, int WAVES, int E>
+__global__ __attribute__((amdgpu_flat_work_group_size(64 * WAVES, 64 * WAVES), amdgpu_waves_per_eu(WAVES / 4)))
 void int8_few(FewArgs a) {
-  using namespace few;
+  constexpr int kWaves = WAVES, kNT = 64 * WAVES, kStep = kFewStep;
   constexpr int kPitch = 4 * NB + 1, kWave = 16 * MF * kPitch;
   __shared__ v4i red[kWaves * kWave];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -672,39 +675,52 @@ void int8_few(FewArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows laid out for tgemm_int8, a wave a row, 16 bytes a lane: as they are, with
-// a length that is whole 16-byte chunks (zeros past the contraction), or decoded
-// from stored codes, a gate's row and an up projection's in turn.
+// Rows laid out for tgemm_int8: as they are, with a length that is whole 16-byte
+// chunks (zeros past the contraction), or decoded from stored codes, a gate's row
+// and an up projection's in turn.  A workgroup takes eight rows, a thread 16 bytes
+// at a time, four loads ahead of their stores.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void lay_rows(const int8_t *__restrict__ src, int8_t *__restrict__ dst, int64_t R,
-                                                int64_t K, int64_t Kp) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= R) return;
-  const int8_t *p = src + row * K;
-  v4i *q = reinterpret_cast<v4i *>(dst + row * Kp);
-  for (int64_t c = threadIdx.x & 63; c < Kp / 16; c += 64) {
-    const int64_t n = K - 16 * c;
-    q[c] = n >= 16 ? v4i(*reinterpret_cast<const v4i_u *>(p + 16 * c)) : load_part(p + 16 * c, n);
+constexpr int kLayT = 256, kLayRows = 8;
+template <class Load>
+__device__ __forceinline__ void lay_out(int8_t *dst, int64_t R, int32_t chunks, Load load) {
+  const int64_t row0 = (int64_t)blockIdx.x * kLayRows;
+  const uint32_t rows = (uint32_t)(R - row0 < kLayRows ? R - row0 : kLayRows), n = rows * (uint32_t)chunks;
+  v4i *q = reinterpret_cast<v4i *>(dst) + row0 * chunks;
+  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += 4 * kLayT) {
+    v4i v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t i = i0 + k * kLayT;
+      if (i < n) v[k] = load(row0 + i / (uint32_t)chunks, i % (uint32_t)chunks);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i0 + k * kLayT < n) q[i0 + k * kLayT] = v[k];
   }
 }
-__global__ __launch_bounds__(256) void lay_gated(const uint8_t *__restrict__ src, int8_t *__restrict__ dst, int64_t N,
-                                                 int64_t K, int64_t Kp) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= 2 * N) return;
-  const uint8_t *p = src + ((row & 1) * N + (row >> 1)) * (K / 4);
-  v4i *q = reinterpret_cast<v4i *>(dst + row * Kp);
-  for (int64_t c = threadIdx.x & 63; c < Kp / 16; c += 64) {
-    const int64_t n = K / 4 - 4 * c;
+__global__ __launch_bounds__(kLayT) void lay_rows(const int8_t *__restrict__ src, int8_t *__restrict__ dst, int64_t R,
+                                                  int64_t K, int32_t chunks) {
+  lay_out(dst, R, chunks, [&](int64_t row, uint32_t c) {
+    const int8_t *p = src + row * K + 16 * c;
+    const int64_t n = K - 16 * (int64_t)c;
+    return n >= 16 ? v4i(*reinterpret_cast<const v4i_u *>(p)) : load_part(p, n);
+  });
+}
+__global__ __launch_bounds__(kLayT) void lay_gated(const uint8_t *__restrict__ src, int8_t *__restrict__ dst, int64_t N,
+                                                   int64_t K, int32_t chunks) {
+  lay_out(dst, 2 * N, chunks, [&](int64_t row, uint32_t c) {
+    const uint8_t *p = src + ((row & 1) * N + (row >> 1)) * (K / 4) + 4 * c;
+    const int64_t n = K / 4 - 4 * (int64_t)c;
     uint32_t x = 0;
     if (n >= 4) {
-      x = *reinterpret_cast<const u32_u *>(p + 4 * c);
+      x = *reinterpret_cast<const u32_u *>(p);
     } else {
 #pragma unroll
       for (int b = 0; b < 3; ++b)
-        if (b < n) x |= (uint32_t)p[4 * c + b] << (8 * b);
+        if (b < n) x |= (uint32_t)p[b] << (8 * b);
     }
-    q[c] = decode16(x);   // code 0 is weight 0
-  }
+    return decode16(x);   // code 0 is weight 0
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -734,7 +750,7 @@ int check_sizes(int64_t M, int64_t N, int64_t K) {
   if (!mul_ok(M, K, &t) || !mul_ok(t, 8, &t) || !mul_ok(N, K, &t) || !mul_ok(t, 8, &t) || !mul_ok(M, N, &t) ||
       !mul_ok(t, 8, &t))
     return TGEMM_ERR_DIM;
-  if (N > kMaxCols || ceil_div(M, 16) * ceil_div(2 * N, 16) > INT32_MAX) return TGEMM_ERR_DIM;
+  if (N > kMaxCols || M / kLayRows > INT32_MAX - 1 || ceil_div(M, 16) * ceil_div(2 * N, 16) > INT32_MAX) return TGEMM_ERR_DIM;
   return TGEMM_OK;
 }
 
@@ -763,31 +779,43 @@ int launch_mm(MArgs a, const Machine &mc, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
 }
 // The tile with the least estimated time: rounds of tiles over the CUs, each of
-// so many us a step and at its end, as measured with every CU at work (fitted to
-// 31 sizes of 65 to 16384 rows; the choice is the fastest of these six or within
-// 2% of it on 27 of them, and 1.7% slower in the mean).  A last round that leaves
-// CUs idle has faster steps; of the two kernels with two workgroups a CU, a last
-// round of one a CU has its own figures.
+// `step` us a step and at its end of `end` us, `out` for each 2 bytes that it moves
+// an output column of the product, and `act` if it takes a sigmoid of each.  A last
+// round that leaves CUs idle has faster steps; of the two kernels with two
+// workgroups a CU, a last round of one a CU has its own figures.  Fitted to 88 calls
+// of 65 to 16384 rows, with and without Z and an activation, bfloat16 and float32:
+// the choice is the fastest of these six or within 2% of it on 67 of them, and 2.6%
+// slower in the mean.  (Rows of less than half a launch's CUs are best with small
+// tiles: 128x4096x4096 takes 11.3 us in 64x64 and 17.6 in 128x128; large outputs with
+// large ones: 16384x6912x1280 takes 141 us in 256x192, 152 in 256x128, 158 in 128x192.)
 struct TileTime {
-  double step, end, step1, end1;
+  double step, end, out, act, step1, end1;
 };
-template <class C>
+template <class C, int E>
 double time_of(const MArgs &a, const Machine &mc, const TileTime &t) {
   const int64_t tiles = ceil_div(a.R, C::BM) * ceil_div(a.Cc, C::BN), slots = (int64_t)mc.cus * C::PERCU;
-  const double steps = (double)ceil_div(a.K, C::KS);
+  const double steps = (double)ceil_div(a.K, C::KS), full = (double)(tiles / slots);
+  const double bytes = (a.o.kind == OUT_BF16 ? 2 : 4) *
+                       (E & EPI_GATED ? 0.5 + (a.o.z ? 1 : 0) : 1.0 + (a.o.z ? 1 : 0) + (a.o.res ? 1 : 0));
+  const double out = bytes / 2, act = (E & kEpiAct) == EPI_SIGM ? (E & EPI_GATED ? 0.5 : 1.0) : 0.0;
   const int64_t rem = tiles % slots;
-  double us = (double)(tiles / slots) * (t.step * steps + t.end);
-  if (rem && C::PERCU == 2 && rem <= mc.cus)
-    us += t.step1 * steps + t.end1;
-  else if (rem)
-    us += t.step * (0.75 + 0.25 * (double)rem / (double)slots) * steps + t.end;
+  double us = full * (t.step * steps + t.end + t.out * out + t.act * act);
+  if (rem && C::PERCU == 2 && rem <= mc.cus) {
+    us += t.step1 * steps + t.end1 * (0.5 + 0.5 * out);
+  } else if (rem) {
+    const double fill = (double)rem / (double)slots;
+    us += t.step * (0.75 + 0.25 * fill) * steps + t.end + t.out * out * fill + t.act * act;
+  }
   return us;
 }
 template <int E>
 int pick_mm(const MArgs &a, const Machine &mc, hipStream_t stream) {
-  const double us[] = {time_of<T256x192>(a, mc, {1.0, 5.4, 0, 0}), time_of<T256x128>(a, mc, {0.82, 3.3, 0, 0}),
-                       time_of<T128x192>(a, mc, {0.6, 2.6, 0, 0}), time_of<T128x128>(a, mc, {0.47, 2.0, 0, 0}),
-                       time_of<T64x128>(a, mc, {0.58, 1.8, 0.34, 1.0}), time_of<T64x64>(a, mc, {0.37, 1.0, 0.2, 0.6})};
+  const double us[] = {time_of<T256x192, E>(a, mc, {1.01, 4.9, 3.1, 2.4, 0, 0}),
+                       time_of<T256x128, E>(a, mc, {0.69, 3.1, 2.4, 1.9, 0, 0}),
+                       time_of<T128x192, E>(a, mc, {0.59, 2.2, 1.9, 1.6, 0, 0}),
+                       time_of<T128x128, E>(a, mc, {0.43, 2.0, 1.0, 1.1, 0, 0}),
+                       time_of<T64x128, E>(a, mc, {0.51, 1.9, 1.0, 0.8, 0.32, 1.1}),
+                       time_of<T64x64, E>(a, mc, {0.33, 1.4, 0.4, 0.5, 0.18, 1.6})};
   int best = 0;
   for (int i = 1; i < 6; ++i)
     if (us[i] < us[best]) best = i;
@@ -806,11 +834,14 @@ int pick_mm_act(const MArgs &a, const Machine &mc, hipStream_t stream) {
 }
 
 void lay(const int8_t *src, int8_t *dst, int64_t R, int64_t K, int64_t Kp, hipStream_t stream) {
-  hipLaunchKernelGGL(lay_rows, dim3((unsigned)ceil_div(R, 4)), dim3(256), 0, stream, src, dst, R, K, Kp);
+  hipLaunchKernelGGL(lay_rows, dim3((unsigned)ceil_div(R, kLayRows)), dim3(kLayT), 0, stream, src, dst, R, K, (int32_t)(Kp / 16));
 }
 
-// few rows go to int8_few, which needs no layout
-constexpr int64_t kFewRows = 64;
+// Few rows go to int8_few, which needs no layout: 32, and up to 64 where the
+// weights are small, or would have to be copied first (48 rows, int8_few against
+// the tiles: 3456x1280 6.0 and 6.4 us, 1280x3456 8.8 and 10.0, but 4096x4096 13.2 and
+// 11.1, 16384x1280 12.7 and 8.7).
+bool few_rows(int64_t M, int64_t N, int64_t K, bool copy) { return M <= 32 || (M <= 64 && (copy || N * K <= 6000000)); }
 
 // the workspace of a call: the rows of either operand laid out anew where they
 // are not whole, aligned 16-byte chunks, those of the gated product's weights always
@@ -825,25 +856,32 @@ Layout layout_of(int64_t M, int64_t rows, int64_t K, bool lay_a, bool lay_w) {
   return l;
 }
 Layout s8s8_layout(int64_t M, int64_t N, int64_t K, int64_t a_align, int64_t w_align) {
-  const bool few = M <= kFewRows, odd = K % 16 != 0;
-  return layout_of(M, N, K, !few && (odd || a_align % 16 != 0), !few && (odd || w_align % 16 != 0));
+  const bool lay_a = K % 16 != 0 || a_align % 16 != 0, lay_w = K % 16 != 0 || w_align % 16 != 0;
+  const bool few = few_rows(M, N, K, lay_a || lay_w);
+  return layout_of(M, N, K, !few && lay_a, !few && lay_w);
 }
 Layout gated_layout(int64_t M, int64_t N, int64_t K, int64_t a_align, int64_t w_align) {
   const bool few = gated_few_ok(M, N, K, min_align(a_align, w_align));
   return layout_of(M, 2 * N, K, !few && (K % 16 != 0 || a_align % 16 != 0), !few);
 }
 
-template <int MF, int NB, int E>
-int launch_few_e(FewArgs a, hipStream_t stream) {
+template <int MF, int NB, int WAVES>
+int launch_few(FewArgs a, hipStream_t stream) {
   a.rblocks = (int32_t)ceil_div(a.M, 16 * MF);
-  hipLaunchKernelGGL((int8_few<MF, NB, E>), dim3((unsigned)(ceil_div(a.N, 16 * NB) * a.rblocks)), dim3(few::kNT), 0,
-                     stream, a);
+  const dim3 grid((unsigned)(ceil_div(a.N, 16 * NB) * a.rblocks)), block(64 * WAVES);
+  if (epi_of(a.o.act) == EPI_POLY)
+    hipLaunchKernelGGL((int8_few<MF, NB, WAVES, EPI_POLY | EPI_COLS>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((int8_few<MF, NB, WAVES, EPI_SIGM | EPI_COLS>), grid, block, 0, stream, a);
   return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
 }
-template <int MF, int NB>
-int launch_few(const FewArgs &a, hipStream_t stream) {
-  return epi_of(a.o.act) == EPI_POLY ? launch_few_e<MF, NB, EPI_POLY | EPI_COLS>(a, stream)
-                                     : launch_few_e<MF, NB, EPI_SIGM | EPI_COLS>(a, stream);
+// column blocks as wide as leaves every CU one, and sixteen waves where a block
+// of 16 has more super-steps than eight
+template <int MF>
+int pick_few(const FewArgs &a, int64_t cus, hipStream_t stream) {
+  if (a.N >= 64 * cus) return launch_few<MF, 4, 8>(a, stream);
+  if (a.N >= 32 * cus) return launch_few<MF, 2, 8>(a, stream);
+  return a.K > 8 * kFewStep ? launch_few<MF, 1, 16>(a, stream) : launch_few<MF, 1, 8>(a, stream);
 }
 
 }  // namespace
@@ -889,15 +927,10 @@ int ternary_gemm_s8s8_epilogue(const int8_t *A, const int8_t *W, const float *a_
   o.res = residual;
   o.z = Z;
   o.act = act;
-  if (M <= kFewRows) {
+  const bool copy = K % 16 != 0 || align_of(A) % 16 != 0 || align_of(W) % 16 != 0;
+  if (few_rows(M, N, K, copy)) {
     const FewArgs a = {A, W, o, M, N, K, 0, mc.xcds};
-    const int64_t half = mc.cus / 2;
-    if (M <= 16) {
-      if (N >= 64 * half) return launch_few<1, 4>(a, stream);
-      return N >= 32 * half ? launch_few<1, 2>(a, stream) : launch_few<1, 1>(a, stream);
-    }
-    if (N >= 64 * half) return launch_few<2, 4>(a, stream);
-    return N >= 32 * half ? launch_few<2, 2>(a, stream) : launch_few<2, 1>(a, stream);
+    return M <= 16 ? pick_few<1>(a, mc.cus, stream) : pick_few<2>(a, mc.cus, stream);
   }
   int8_t *la = static_cast<int8_t *>(workspace), *lw = la + l.a_bytes;
   if (l.a_bytes) lay(A, la, M, K, l.kp, stream);
@@ -941,7 +974,8 @@ int ternary_gemm_s8_gated(const int8_t *A, const uint8_t *Wpacked, const float *
                      stream);
   int8_t *la = static_cast<int8_t *>(workspace), *lw = la + l.a_bytes;
   if (l.a_bytes) lay(A, la, M, K, l.kp, stream);
-  hipLaunchKernelGGL(lay_gated, dim3((unsigned)ceil_div(2 * N, 4)), dim3(256), 0, stream, Wpacked, lw, N, K, l.kp);
+  hipLaunchKernelGGL(lay_gated, dim3((unsigned)ceil_div(2 * N, kLayRows)), dim3(kLayT), 0, stream, Wpacked, lw, N, K,
+                     (int32_t)(l.kp / 16));
   Out o{};
   o.ptr = Y;
   o.rs = a_row_scale;

@@ -469,10 +469,9 @@ __device__ __forceinline__ v4i decode16(uint32_t x) {
 
 }  // namespace
 
-// The gated product of at most kGatedFewRows rows on the stored codes, in
-// ternary_gemm.hip: whether it takes these sizes and this smallest alignment of
-// A and Wpacked, and the call (arguments checked by the caller).
-constexpr int64_t kGatedFewRows = 64;
+// The gated product of few rows on the stored codes, in ternary_gemm.hip: whether
+// it takes these sizes and this smallest alignment of A and Wpacked, and the call
+// (arguments checked by the caller).
 struct GatedCall {
   const int8_t *A;
   const uint8_t *Wpacked;

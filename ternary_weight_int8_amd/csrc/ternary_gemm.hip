@@ -2816,8 +2816,13 @@ void launch_gated_few(const KArgs &ka, dim3 grid, hipStream_t stream) {
 
 }  // namespace
 
+// Each block of 32 rows decodes the weights anew, which the tiles of int8.hip do once
+// in a launch of its own: up to 128 rows, or 192 of at most 8192 columns (us, few
+// rows against tiles: 3456x1280, 128 rows 10.1 and 13.4, 192 14.1 and 15.6, 256 16.8
+// and 15.8; 4096x4096 16.0 and 24.5, 22.7 and 27.7, 29.5 and 27.7; 16384x1280 31.2 and 30.6,
+// 44.5 and 34.1).
 bool gated_few_ok(int64_t M, int64_t N, int64_t K, int64_t align) {
-  return M <= kGatedFewRows && K % 64 == 0 && align % 16 == 0 && N <= (INT32_MAX - 64) / 2 && K <= INT32_MAX;
+  return (M <= 128 || (M <= 192 && N <= 8192)) && K % 64 == 0 && align % 16 == 0 && N <= (INT32_MAX - 64) / 2 && K <= INT32_MAX;
 }
 
 int gated_few(const GatedCall &c, int32_t cus, int32_t xcds, hipStream_t stream) {
