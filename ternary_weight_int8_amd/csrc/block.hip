@@ -480,6 +480,31 @@ __device__ __forceinline__ void write_cols(float (&acc)[V][kU<T>], const Units<T
   }
 }
 
+// The same by one workgroup for all rows (the passes with two column sums): every
+// group's sums lie side by side in LDS, and the threads each add columns up, group
+// after group, which takes no turns of the groups.
+constexpr int kOneGroups = 16;
+template <class T, int V>
+__device__ __forceinline__ void write_cols_one(float (&acc)[V][kU<T>], const Units<T, 1, V> &un, int grp, int32_t C,
+                                               float *lds, float *__restrict__ out) {
+  constexpr int U = kU<T>;
+  __syncthreads();   // the sums before these have been read
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (un.on(j)) {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (j != un.last || i >= un.dup) lds[grp * (64 * V * U) + un.off[j] + i] = acc[j][i];
+    }
+  __syncthreads();
+  const int groups = (int)(blockDim.x >> 6);
+  for (int32_t c = threadIdx.x; c < C; c += blockDim.x) {
+    float sum = lds[c];
+    for (int g = 1; g < groups; ++g) sum += lds[g * (64 * V * U) + c];
+    out[c] = sum;
+  }
+}
+
 struct NormBwdArgs {
   const void *dY, *H;
   const float *gain, *rstd;
@@ -967,11 +992,11 @@ __device__ __forceinline__ f32x2 row_sum2(float v, float w, f32x2 *part) {
   return f32x2{v, w};
 }
 
-template <class T, int W, int V>
-__global__ __launch_bounds__(max_t(W, V)) void ln_bwd_reg(LnBwdArgs a) {
+template <class T, int W, int V, bool ONE = false>
+__global__ __launch_bounds__(ONE ? 64 * kOneGroups : max_t(W, V)) void ln_bwd_reg(LnBwdArgs a) {
   constexpr int U = kU<T>;
   __shared__ f32x2 part[2][16];
-  __shared__ float cols[W ? 64 * V * U : 1];
+  __shared__ float cols[ONE ? kOneGroups * 64 * V * U : W ? 64 * V * U : 1];
   const int t = W ? threadIdx.x & 63 : threadIdx.x;
   const int grp = W ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   Units<T, W, V> un;
@@ -1057,8 +1082,13 @@ __global__ __launch_bounds__(max_t(W, V)) void ln_bwd_reg(LnBwdArgs a) {
         store_raw(static_cast<T *>(a.dX) + base + un.off[j], pack(d));
       }
   }
-  write_cols<T, W, V>(acc, un, grp, cols, a.P + (int64_t)blockIdx.x * a.pitch);
-  if (a.P2) write_cols<T, W, V>(bacc, un, grp, cols, a.P2 + (int64_t)blockIdx.x * a.pitch);
+  if constexpr (ONE) {
+    write_cols_one<T, V>(acc, un, grp, (int32_t)a.C, cols, a.P);
+    if (a.P2) write_cols_one<T, V>(bacc, un, grp, (int32_t)a.C, cols, a.P2);
+  } else {
+    write_cols<T, W, V>(acc, un, grp, cols, a.P + (int64_t)blockIdx.x * a.pitch);
+    if (a.P2) write_cols<T, W, V>(bacc, un, grp, cols, a.P2 + (int64_t)blockIdx.x * a.pitch);
+  }
 }
 
 template <class T>
@@ -1125,11 +1155,11 @@ __device__ __forceinline__ f32x2 gated_back(float dy, float z, float u, int act)
   return is_sigm(act) ? gated_sigm(dy, z, u, sigm_of(act)) : gated_poly(dy, z, u, act);
 }
 
-template <class T, int W, int V, int S>
-__global__ __launch_bounds__(max_t(W, V)) void gated_bwd_reg(GatedBwdArgs a) {
+template <class T, int W, int V, int S, bool ONE = false>
+__global__ __launch_bounds__(ONE ? 64 * kOneGroups : max_t(W, V)) void gated_bwd_reg(GatedBwdArgs a) {
   constexpr int U = kU<T>;
   __shared__ uint32_t upart[2][16];
-  __shared__ float cols[W ? 64 * V * U : 1];
+  __shared__ float cols[ONE ? kOneGroups * 64 * V * U : W ? 64 * V * U : 1];
   const int t = W ? threadIdx.x & 63 : threadIdx.x;
   const int grp = W ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   Units<T, W, V> un;
@@ -1192,7 +1222,12 @@ __global__ __launch_bounds__(max_t(W, V)) void gated_bwd_reg(GatedBwdArgs a) {
         store_q<U>(a.Q + zbase + a.C + un.off[j], du[j], s, r, fast);
       }
   }
-  if (a.P) {
+  if constexpr (ONE) {
+    if (a.P) {
+      write_cols_one<T, V>(zacc, un, grp, (int32_t)a.C, cols, a.P);
+      write_cols_one<T, V>(uacc, un, grp, (int32_t)a.C, cols, a.P + a.C);
+    }
+  } else if (a.P) {
     float *P = a.P + (int64_t)blockIdx.x * 2 * a.C;
     write_cols<T, W, V>(zacc, un, grp, cols, P);
     write_cols<T, W, V>(uacc, un, grp, cols, P + a.C);
@@ -1587,6 +1622,9 @@ ROW_KERNEL(LnReg, false, LnArgs, ln_reg<T, W, V>)
 ROW_KERNEL(LnBwdReg, true, LnBwdArgs, ln_bwd_reg<T, W, V>)
 ROW_KERNEL(GatedBwdPoly, true, GatedBwdArgs, gated_bwd_reg<T, W, V, 0>)
 ROW_KERNEL(GatedBwdSigm, true, GatedBwdArgs, gated_bwd_reg<T, W, V, 1>)
+ROW_KERNEL(LnBwdOne, true, LnBwdArgs, ln_bwd_reg<T, W, V, true>)
+ROW_KERNEL(GatedBwdPolyOne, true, GatedBwdArgs, gated_bwd_reg<T, W, V, 0, true>)
+ROW_KERNEL(GatedBwdSigmOne, true, GatedBwdArgs, gated_bwd_reg<T, W, V, 1, true>)
 #undef ROW_KERNEL
 template <class Kernel>
 void row_launch(int kind, const RowPlan &p, const typename Kernel::Args &a, hipStream_t stream) {
@@ -1594,6 +1632,42 @@ void row_launch(int kind, const RowPlan &p, const typename Kernel::Args &a, hipS
     row_launch<Kernel, float>(p, a, stream);
   else
     row_launch<Kernel, uint16_t>(p, a, stream);
+}
+
+// The passes with two column sums: their plan is row_plan's but for few rows, which
+// one workgroup takes, up to three units a lane in float32 and two in bfloat16 (three
+// spill): ONE_TIMES
+constexpr int64_t kOneRows = 32;
+bool one_ok(int64_t R, int64_t C, int kind) {
+  const int U = kind == TGEMM_IN_F32 ? kU<float> : kU<uint16_t>;
+  return R <= kOneRows && C >= U && ceil_div(C, U) <= (kind == TGEMM_IN_F32 ? 192 : 128);
+}
+template <class Kernel, class T>
+void one_launch(int64_t R, int64_t C, const typename Kernel::Args &a, hipStream_t stream) {
+  const dim3 g(1), b((unsigned)(64 * (R < kOneGroups ? R : kOneGroups)));
+  switch (ceil_div(ceil_div(C, kU<T>), 64)) {
+    case 1: hipLaunchKernelGGL((Kernel::template Of<T, 1, 1>::run), g, b, 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((Kernel::template Of<T, 1, 2>::run), g, b, 0, stream, a); break;
+    default:
+      if constexpr (kU<T> == 4) hipLaunchKernelGGL((Kernel::template Of<T, 1, 3>::run), g, b, 0, stream, a);
+      break;
+  }
+}
+template <class Kernel>
+void one_launch(int kind, int64_t R, int64_t C, const typename Kernel::Args &a, hipStream_t stream) {
+  if (kind == TGEMM_IN_F32)
+    one_launch<Kernel, float>(R, C, a, stream);
+  else
+    one_launch<Kernel, uint16_t>(R, C, a, stream);
+}
+int64_t two_sums_ws_bytes(int64_t R, int64_t C) {
+  int64_t rows = 0;
+  for (const int kind : {TGEMM_IN_F32, TGEMM_IN_BF16}) {
+    const RowPlan p = row_plan(R, C, kind, true);
+    const int64_t n = one_ok(R, C, kind) ? 0 : p.v == 0 ? strips_of(R) : p.grid;
+    rows = n > rows ? n : rows;
+  }
+  return 4 * rows * 2 * C;
 }
 
 // bytes of P for either kind: a row for each workgroup of the row kernel, or
@@ -1782,7 +1856,7 @@ int ternary_layernorm_backward_workspace(int64_t R, int64_t C, int64_t *bytes) {
   if (!bytes) return TGEMM_ERR_NULL;
   const int st = check_rc(TGEMM_IN_F32, R, C);
   if (st != TGEMM_OK) return st;
-  *bytes = 2 * col_ws_bytes(R, C);
+  *bytes = two_sums_ws_bytes(R, C);
   return TGEMM_OK;
 }
 
@@ -1792,7 +1866,7 @@ int ternary_layernorm_backward(const void *dY, const void *H, int in_kind, const
   if (!dY || !H || !gain || !mean || !rstd || !dX || !dgain) return TGEMM_ERR_NULL;
   const int st = check_rc(in_kind, R, C);
   if (st != TGEMM_OK) return st;
-  if (!workspace_ok(workspace, workspace_bytes, 2 * col_ws_bytes(R, C))) return TGEMM_ERR_WORKSPACE;
+  if (!workspace_ok(workspace, workspace_bytes, two_sums_ws_bytes(R, C))) return TGEMM_ERR_WORKSPACE;
   const int64_t xb = R * C * (in_kind == TGEMM_IN_F32 ? 4 : 2);
   const Buf outs[] = {{dX, xb}, {dgain, 4 * C}, {dbeta, 4 * C}, {workspace, workspace_bytes > 0 ? workspace_bytes : 0}};
   const Buf ins[] = {{dY, xb}, {H, xb}, {gain, 4 * C}, {mean, 4 * R}, {rstd, 4 * R}, {dH, xb}};
@@ -1800,14 +1874,16 @@ int ternary_layernorm_backward(const void *dY, const void *H, int in_kind, const
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
   float *P = static_cast<float *>(workspace);
   LnBwdArgs a = {dY, H, gain, mean, rstd, dH, dX, P, dbeta ? P + C : nullptr, dbeta ? 2 * C : C, R, C};
+  if (one_ok(R, C, in_kind)) {
+    a.P = dgain;
+    a.P2 = dbeta;
+    one_launch<LnBwdOne>(in_kind, R, C, a, stream);
+    return done();
+  }
   const RowPlan p = row_plan(R, C, in_kind, true);
   if (p.v) {
-    if (p.grid == 1) {
-      a.P = dgain;
-      a.P2 = dbeta;
-    }
     row_launch<LnBwdReg>(in_kind, p, a, stream);
-    if (p.grid > 1) launch_finish2(P, dgain, dbeta, p.grid, C, stream);
+    launch_finish2(P, dgain, dbeta, p.grid, C, stream);
     return done();
   }
   const dim3 g((unsigned)(R < kMaxRowGrid ? R : kMaxRowGrid));
@@ -1830,7 +1906,7 @@ int ternary_gated_backward(const void *dY, const void *Z, int in_kind, int act, 
   const int st = check_rc(in_kind, R, C);
   if (st != TGEMM_OK) return st;
   if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_VALUE;
-  const int64_t wb = dbias ? 2 * col_ws_bytes(R, C) : 0;
+  const int64_t wb = dbias ? two_sums_ws_bytes(R, C) : 0;
   if (!workspace_ok(workspace, workspace_bytes, wb)) return TGEMM_ERR_WORKSPACE;
   const int64_t n = R * C, xb = n * (in_kind == TGEMM_IN_F32 ? 4 : 2);
   const Buf outs[] = {{dZ, 2 * xb}, {dbias, 8 * C}, {Q, 2 * n}, {scale, 4 * R},
@@ -1840,14 +1916,21 @@ int ternary_gated_backward(const void *dY, const void *Z, int in_kind, int act, 
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
   float *P = static_cast<float *>(workspace);
   GatedBwdArgs a = {dY, Z, dZ, Q, scale, dbias ? P : nullptr, gate_scale, up_scale, R, C, act};
+  if (one_ok(R, C, in_kind)) {
+    a.P = dbias;
+    if (is_sigm(act))
+      one_launch<GatedBwdSigmOne>(in_kind, R, C, a, stream);
+    else
+      one_launch<GatedBwdPolyOne>(in_kind, R, C, a, stream);
+    return done();
+  }
   const RowPlan p = row_plan(R, C, in_kind, true);
   if (p.v) {
-    if (p.grid == 1) a.P = dbias;
     if (is_sigm(act))
       row_launch<GatedBwdSigm>(in_kind, p, a, stream);
     else
       row_launch<GatedBwdPoly>(in_kind, p, a, stream);
-    if (dbias && p.grid > 1) launch_finish(P, dbias, p.grid, 2 * C, stream);
+    if (dbias) launch_finish(P, dbias, p.grid, 2 * C, stream);
     return done();
   }
   const dim3 g((unsigned)(R < kMaxRowGrid ? R : kMaxRowGrid));
