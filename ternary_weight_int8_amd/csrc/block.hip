@@ -1635,12 +1635,19 @@ void row_launch(int kind, const RowPlan &p, const typename Kernel::Args &a, hipS
 }
 
 // The passes with two column sums: their plan is row_plan's but for few rows, which
-// one workgroup takes, up to three units a lane in float32 and two in bfloat16 (three
-// spill): ONE_TIMES
-constexpr int64_t kOneRows = 32;
-bool one_ok(int64_t R, int64_t C, int kind) {
-  const int U = kind == TGEMM_IN_F32 ? kU<float> : kU<uint16_t>;
-  return R <= kOneRows && C >= U && ceil_div(C, U) <= (kind == TGEMM_IN_F32 ? 192 : 128);
+// one workgroup takes (write_cols_one), up to three units a lane in float32 and two
+// in bfloat16 (three spill).  That saves the second launch and the workspace: the
+// norm, 27x729 f32, 11.4 against 15.9 us a call (8.3 against 5.6 in a graph), 27x243
+// 11.4 and 16.0 (4.5 and 6.4), 32x1000 bf16 13.5 and 16.1 (10.9 and 6.1).  The gated
+// pass has several times the instructions, and one CU for all of them: past two units
+// a lane in float32 and one in bfloat16 it is so up to 16 rows, where the GPU takes as
+// long as the host (16x729 f32 12.8 us a call against 17.0, 12.4 against 5.9 in a graph;
+// 27 rows 14.9 and 15.2, 32 rows 17.3 and 17.6).
+bool one_ok(int64_t R, int64_t C, int kind, bool gated) {
+  const bool f32 = kind == TGEMM_IN_F32;
+  const int64_t U = f32 ? kU<float> : kU<uint16_t>, units = ceil_div(C, U);
+  if (C < U || units > (f32 ? 192 : 128)) return false;
+  return R <= (gated && units > (f32 ? 128 : 64) ? 16 : 32);
 }
 template <class Kernel, class T>
 void one_launch(int64_t R, int64_t C, const typename Kernel::Args &a, hipStream_t stream) {
@@ -1660,11 +1667,11 @@ void one_launch(int kind, int64_t R, int64_t C, const typename Kernel::Args &a, 
   else
     one_launch<Kernel, uint16_t>(R, C, a, stream);
 }
-int64_t two_sums_ws_bytes(int64_t R, int64_t C) {
+int64_t two_sums_ws_bytes(int64_t R, int64_t C, bool gated) {
   int64_t rows = 0;
   for (const int kind : {TGEMM_IN_F32, TGEMM_IN_BF16}) {
     const RowPlan p = row_plan(R, C, kind, true);
-    const int64_t n = one_ok(R, C, kind) ? 0 : p.v == 0 ? strips_of(R) : p.grid;
+    const int64_t n = one_ok(R, C, kind, gated) ? 0 : p.v == 0 ? strips_of(R) : p.grid;
     rows = n > rows ? n : rows;
   }
   return 4 * rows * 2 * C;
@@ -1856,7 +1863,7 @@ int ternary_layernorm_backward_workspace(int64_t R, int64_t C, int64_t *bytes) {
   if (!bytes) return TGEMM_ERR_NULL;
   const int st = check_rc(TGEMM_IN_F32, R, C);
   if (st != TGEMM_OK) return st;
-  *bytes = two_sums_ws_bytes(R, C);
+  *bytes = two_sums_ws_bytes(R, C, false);
   return TGEMM_OK;
 }
 
@@ -1866,7 +1873,7 @@ int ternary_layernorm_backward(const void *dY, const void *H, int in_kind, const
   if (!dY || !H || !gain || !mean || !rstd || !dX || !dgain) return TGEMM_ERR_NULL;
   const int st = check_rc(in_kind, R, C);
   if (st != TGEMM_OK) return st;
-  if (!workspace_ok(workspace, workspace_bytes, two_sums_ws_bytes(R, C))) return TGEMM_ERR_WORKSPACE;
+  if (!workspace_ok(workspace, workspace_bytes, two_sums_ws_bytes(R, C, false))) return TGEMM_ERR_WORKSPACE;
   const int64_t xb = R * C * (in_kind == TGEMM_IN_F32 ? 4 : 2);
   const Buf outs[] = {{dX, xb}, {dgain, 4 * C}, {dbeta, 4 * C}, {workspace, workspace_bytes > 0 ? workspace_bytes : 0}};
   const Buf ins[] = {{dY, xb}, {H, xb}, {gain, 4 * C}, {mean, 4 * R}, {rstd, 4 * R}, {dH, xb}};
@@ -1874,7 +1881,7 @@ int ternary_layernorm_backward(const void *dY, const void *H, int in_kind, const
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
   float *P = static_cast<float *>(workspace);
   LnBwdArgs a = {dY, H, gain, mean, rstd, dH, dX, P, dbeta ? P + C : nullptr, dbeta ? 2 * C : C, R, C};
-  if (one_ok(R, C, in_kind)) {
+  if (one_ok(R, C, in_kind, false)) {
     a.P = dgain;
     a.P2 = dbeta;
     one_launch<LnBwdOne>(in_kind, R, C, a, stream);
@@ -1896,7 +1903,11 @@ int ternary_layernorm_backward(const void *dY, const void *H, int in_kind, const
 }
 
 int ternary_gated_backward_workspace(int64_t R, int64_t C, int64_t *bytes) {
-  return ternary_layernorm_backward_workspace(R, C, bytes);
+  if (!bytes) return TGEMM_ERR_NULL;
+  const int st = check_rc(TGEMM_IN_F32, R, C);
+  if (st != TGEMM_OK) return st;
+  *bytes = two_sums_ws_bytes(R, C, true);
+  return TGEMM_OK;
 }
 
 int ternary_gated_backward(const void *dY, const void *Z, int in_kind, int act, float gate_scale, float up_scale,
@@ -1906,7 +1917,7 @@ int ternary_gated_backward(const void *dY, const void *Z, int in_kind, int act, 
   const int st = check_rc(in_kind, R, C);
   if (st != TGEMM_OK) return st;
   if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_VALUE;
-  const int64_t wb = dbias ? two_sums_ws_bytes(R, C) : 0;
+  const int64_t wb = dbias ? two_sums_ws_bytes(R, C, true) : 0;
   if (!workspace_ok(workspace, workspace_bytes, wb)) return TGEMM_ERR_WORKSPACE;
   const int64_t n = R * C, xb = n * (in_kind == TGEMM_IN_F32 ? 4 : 2);
   const Buf outs[] = {{dZ, 2 * xb}, {dbias, 8 * C}, {Q, 2 * n}, {scale, 4 * R},
@@ -1916,7 +1927,7 @@ int ternary_gated_backward(const void *dY, const void *Z, int in_kind, int act, 
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
   float *P = static_cast<float *>(workspace);
   GatedBwdArgs a = {dY, Z, dZ, Q, scale, dbias ? P : nullptr, gate_scale, up_scale, R, C, act};
-  if (one_ok(R, C, in_kind)) {
+  if (one_ok(R, C, in_kind, true)) {
     a.P = dbias;
     if (is_sigm(act))
       one_launch<GatedBwdSigmOne>(in_kind, R, C, a, stream);

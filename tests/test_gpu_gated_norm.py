@@ -97,7 +97,7 @@ def test_layernorm_of_a_mean_far_larger_than_the_deviation():
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("R,C", ROWS + [(1782, 729), (600, 3456), (32, 64), (33, 64)])
+@pytest.mark.parametrize("R,C", ROWS + [(1782, 729), (600, 3456), (32, 64), (33, 64), (17, 500), (32, 766), (19, 1022)])
 def test_layernorm_backward(R, C, kind):
     say(f"layernorm backward {R}x{C} {kind}")
     dt, g = KINDS[kind], gen("lnb", R, C, kind)
@@ -128,7 +128,7 @@ def test_layernorm_backward(R, C, kind):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("R,C", [(1, 1), (1, 3), (3, 7), (27, 243), (65, 511), (5, 513), (32, 512), (33, 512), (200, 729),
+@pytest.mark.parametrize("R,C", [(1, 1), (1, 3), (3, 7), (27, 243), (65, 511), (5, 513), (32, 512), (33, 512), (16, 729), (17, 729), (9, 1001), (200, 729),
                                  (130, 3456), (7, 4104), (3, 8191), (4, 8200), (2, 16384), (3, 16401), (2500, 64)])
 def test_gated_backward(R, C, kind, act):
     say(f"gated backward {R}x{C} {kind} {act}")
