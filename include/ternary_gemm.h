@@ -364,7 +364,8 @@ int ternary_epilogue_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
  *     h = x + residual       rounded to the kind (h = x without a residual)
  *     mean = sum_c h / C,  rstd = 1 / sqrt(sum_c (h - mean)^2 / C + eps)
  *     y = ((h - mean) * rstd) * gain[c] + beta[c]
- * and Q, scale from y.  Arguments, checks and in-place forms are those of
+ * and Q, scale from y.  With eps = 0 a row of one value has rstd = inf and
+ * y = NaN, as the formula does.  Arguments, checks and in-place forms are those of
  * ternary_rmsnorm_quantize, and
  *   beta        float [C], or NULL for 0
  *   mean, rstd  float [R] each, or both NULL (the backward pass takes them)
@@ -401,6 +402,7 @@ int ternary_layernorm_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
  * Any K up to TGEMM_INT8_MAX_CONTRACTION (TGEMM_ERR_BOUND).  Its gradients: dX is
  * this call on dZ's int8 rows and the transposed weights, quantized row by row
  * like the weights; dW is ternary_gemm_s8_dw_scaled on both operands' columns.
+ * N is at most 2^29 (TGEMM_ERR_DIM).
  * Workspace: where K is not a multiple of 16 or an operand's base not 16-byte
  * aligned, more than 64 rows need it (operands are copied into aligned rows).
  * The query takes the smallest alignment of A and W, in bytes.
@@ -425,6 +427,7 @@ int ternary_gemm_s8s8_workspace(int64_t M, int64_t N, int64_t K, int64_t align, 
  *   bias     float [2N], or NULL
  *   Y        [M][N] of out_kind
  *   Z        [M][2N] of out_kind, (g | u) for ternary_gated_backward, or NULL
+ * The checks of ternary_gemm_s8_epilogue; N is at most 2^29 (TGEMM_ERR_DIM).
  * Workspace: more than 128 to 192 rows need one (the weights' codes are decoded
  * into it, 2 N K bytes), and so do fewer where K is not a multiple of 64 or A or
  * Wpacked not 16-byte aligned.  The query takes their smallest alignment, in bytes.

@@ -15,6 +15,39 @@
 
 namespace {
 
+// ---------------------------------------------------------------------------
+// Tiled kernel (tgemm_int8): both operands are int8 rows along the contraction, of
+// whole 16-byte chunks, 16-byte aligned; K products a row are counted, the rest of
+// the last step as zeros.  (Ternary weights come decoded, see lay_gated: decoding in
+// the tile's own loop costs its waves 16 vector instructions a fragment, and the
+// ternary kernels have a barrier every 64 values: 4096x1280x3456 takes tgemm_ring 37 us,
+// float32 with a residual, and this kernel 23, bfloat16 without.)
+//
+// Persistent workgroups of NW = WM x WN waves, one or two a CU, take tiles of BM x BN
+// in XCD-contiguous order, in bands of columns.  A step is KS = 128 values: a row's
+// 128 bytes are a whole line, and the loads go straight into LDS, into a ring of D
+// stages.  Chunk c of row r lies at slot c ^ ((r >> 1) & 7), free of conflicts for the
+// fragment reads (16 rows at one chunk) and, the loads' lanes taking slots in order,
+// for the loads.  A step has U = 2 substeps of one v_mfma_i32_16x16x64_i8 a fragment
+// pair; during one, the fragments of the next are read.  The step's one barrier
+// stands before its last substep: by then every wave has read all of stage g, so the
+// loads of step g + D go into it from there on, and the barrier publishes stage g + 1,
+// which the last substep reads from.  A wave waits there for its own loads of step
+// g + 1, that is until at most the D - 2 batches after them are in flight.
+//
+// What bounds it: a tile reads (BM + BN) KS bytes a step through the CU's vector
+// memory pipe for 2 BM BN KS operations, and the waves of a SIMD do not hide all of
+// that, nor the barrier, under each other's products (16384x6912x5120: 2.53 POP/s in 256
+// x 192, 2.25 in 256 x 128, 1.9 in 128 x 128; without loads 2.7, without loads and LDS
+// reads 3.2, at which the card's power limit lowers the clock); and the tile ends, whose
+// stores all CUs make at once while no products run (226 MB of bfloat16 take some 50 us
+// of 16384x6912x1280's 154).  256 x 192 is the largest tile whose sums (96 registers) and
+// two sets of fragments (80) leave room: 256 x 256 spills.  Tried and left out: the tile
+// before written during the next one's first steps, its sums set aside (33 to 49
+// registers spill, 126 -> 166 us); a wave's priority raised for its products (+4%);
+// lines touched steps ahead for the L2s (+30%: a touch costs the pipe as much as a
+// load); steps of 64 (half lines, +10%); starts of the CUs apart (no change).
+// ---------------------------------------------------------------------------
 namespace mm {
 template <int BM_, int BN_, int WM_, int WN_, int KS_, int D_, int PERCU_>
 struct Cfg {
@@ -39,9 +72,9 @@ struct Flag {
 };
 
 struct MArgs {
-  const int8_t *A, *W;
+  const int8_t *A, *W;   // rows of the output, rows of its columns
   Out o;
-  int64_t R, Cc, K;
+  int64_t R, Cc, K;      // rows, columns, row length in bytes (a multiple of 16)
   int32_t tiles_r, tiles_c, tiles, band_cols, xcds;
   int32_t nk;     // steps
   int32_t tail;   // 16-byte chunks of the last step
@@ -50,9 +83,9 @@ struct MArgs {
 // ---------------------------------------------------------------------------
 // A tile's output.  Scales and biases come from LDS, where the tile's loads have
 // put them: a global load here would wait for the stores before it, since a
-// wave's memory operations complete in order (with such loads the end of a 256 x
-// 128 tile took 6 us, and 16384x6912x1280 bf16 187 us).  For the same reason a residual
-// is read a fragment row ahead, before the stores of the row in hand.
+// wave's memory operations complete in order (1782x3456x1280 bf16 took 19.1 us with
+// such loads and 16.4 without).  For the same reason a residual is read a fragment row
+// ahead, before the stores of the row in hand.
 //   aux: BM row scales, then BN column scales (COLS) or nothing, then BN biases
 // A fragment row goes out as in epi_run: bfloat16 fragments in pairs, 16 bytes a
 // lane, four lanes 64 bytes of a row; float32 16 bytes a lane, 64 a row.
@@ -323,6 +356,9 @@ void tgemm_int8(MArgs a) {
     n0 = (int64_t)tc * C::BN;
   };
 
+  // A wave's load i fills the RPL rows from RPL (kALoads wave + i) on, lane l slot
+  // l % CH of row l / CH; offsets are from the tile's first row, 255 rows of 16 MB at
+  // most.  Rows past the output load the last one again (computed, never stored).
   uint32_t offA[C::kALoads], offW[C::kWLoads];
   const int8_t *ab, *wb;
   const int lrow = lane / C::CH, lslot = lane % C::CH;
@@ -335,12 +371,12 @@ void tgemm_int8(MArgs a) {
 #pragma unroll
     for (int i = 0; i < C::kALoads; ++i) {
       const int r = C::RPL * (C::kALoads * wave + i) + lrow;
-      offA[i] = (uint32_t)((r < mr ? r : mr) * (int32_t)a.K + 16 * (lslot ^ ((r >> 1) & (C::CH - 1))));
+      offA[i] = (uint32_t)(r < mr ? r : mr) * (uint32_t)a.K + 16 * (uint32_t)(lslot ^ ((r >> 1) & (C::CH - 1)));
     }
 #pragma unroll
     for (int i = 0; i < C::kWLoads; ++i) {
       const int r = C::RPL * (C::kWLoads * wave + i) + lrow;
-      offW[i] = (uint32_t)((r < nr ? r : nr) * (int32_t)a.K + 16 * (lslot ^ ((r >> 1) & (C::CH - 1))));
+      offW[i] = (uint32_t)(r < nr ? r : nr) * (uint32_t)a.K + 16 * (uint32_t)(lslot ^ ((r >> 1) & (C::CH - 1)));
     }
   };
   // the last step's chunks past the contraction load its last one again
@@ -396,6 +432,7 @@ void tgemm_int8(MArgs a) {
              4 * ((uint32_t)(at < left ? at : left - 1) + half), src);
     }
   };
+  // load cursor: the next step whose loads go out; past the end it stays on the last
   int32_t it_ld = 0, s_ld = 0;
   auto next_load = [&]() {
     if (s_ld + 1 < a.nk) {
@@ -541,6 +578,9 @@ void tgemm_int8(MArgs a) {
 // takes 64 bytes of 16 rows, and q = 0 .. 3 are the four MFMA steps of the
 // super-step.  Any contraction and any alignment: loads are byte-aligned
 // vectors, and the last, partial super-step reads the bytes inside one by one.
+// Bound by reading the weights and, where they are few, by one round trip to memory:
+// 1x16384x1280 6.2 us in a graph (21 MB), 1x4096x4096 5.6 us, 1x16384x4096 16.0 us (4.2 TB/s),
+// 27 rows of it 19.9 us, A coming from the L2s for every column block.
 // ---------------------------------------------------------------------------
 constexpr int kFewStep = 256;
 typedef int32_t v4i_u __attribute__((ext_vector_type(4), aligned(1)));
@@ -767,6 +807,7 @@ int launch_mm(MArgs a, const Machine &mc, hipStream_t stream) {
   a.tiles_c = (int32_t)ceil_div(a.Cc, C::BN);
   a.tiles = a.tiles_r * a.tiles_c;
   a.xcds = mc.xcds;
+  // an XCD's tiles in flight, 8 columns wide: 16384x6912x1280 141 us, 16 wide 147, 4 144, 2 150
   a.band_cols = a.tiles_c < 8 ? a.tiles_c : 8;
   a.nk = (int32_t)ceil_div(a.K, C::KS);
   a.tail = (int32_t)((a.K - (int64_t)(a.nk - 1) * C::KS) / 16);
