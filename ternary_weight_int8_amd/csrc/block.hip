@@ -858,7 +858,7 @@ template <class T, int W, int V>
 __global__ __launch_bounds__(max_t(W, V)) void ln_reg(LnArgs a) {
   constexpr int U = kU<T>;
   // In float32 a workgroup's next row is loaded while it reduces the one in hand
-  // (16384x3456 with residual 177 -> 149 us, without 139 -> 131; four units a lane spill).
+  // (16384x3456 at one unit a lane, residual 177 -> 149 us, without 139 -> 131; four units spill).
   // bfloat16 rows gain nothing from it without a residual and lose with one (89 -> 97 us).
   constexpr bool kAhead = W == 0 && U == 4 && V <= 3;
   __shared__ float part[2][16], part2[2][16];
@@ -1614,6 +1614,30 @@ RowPlan row_plan(int64_t R, int64_t C, int kind, bool sums) {
   return p;
 }
 
+// The layer norm's plan: a row's fixed work (the steps of its three reductions,
+// its barriers) is done by every wave of it, so past 256 units a row takes the
+// fewest waves that its registers allow, of a number that fills the 16 waves of a
+// CU with whole rows. bfloat16: two units a thread but where that is six waves (12
+// of 16): 16384x3456 70 -> 50 us (with residual and Y 115 -> 98), 8000x7000 84 ->
+// 53, 8000x5000 (five waves) equal, 6000x6000 (six) 45 -> 49 and left. float32:
+// three units, but two where those are four, seven or eight waves and three would
+// be three, five or six: 16384x1280 52 -> 29 us at three and 32 at two, 8000x2000
+// 34 -> 21 and 19, 10000x2600 65 -> 31 and 47, 16384x3456 129 -> 87 and 76.
+RowPlan ln_plan(int64_t R, int64_t C, int kind) {
+  RowPlan p = row_plan(R, C, kind, false);
+  const bool f32 = kind == TGEMM_IN_F32;
+  const int64_t nu = ceil_div(C, f32 ? kU<float> : kU<uint16_t>);
+  if (!p.v || p.w || nu <= 256) return p;
+  const int v = !f32 || (nu > 384 && nu <= 512) || (nu > 768 && nu <= 1024) ? 2 : 3;
+  const int waves = (int)ceil_div(nu, 64 * v);
+  if (v <= p.v || (!f32 && waves == 6)) return p;
+  p.v = v;
+  p.bt = 64 * waves;
+  const int64_t per = kNormWaves / waves, cap = kCUs * (per > 1 ? per : 1);
+  p.grid = R < cap ? R : cap;
+  return p;
+}
+
 // the row kernel K<T, W, V> of a plan
 #define ROW_CASE(W, V) \
   case W * 8 + V: hipLaunchKernelGGL((Kernel::template Of<T, W, V>::run), g, b, 0, stream, a); break;
@@ -1879,7 +1903,7 @@ int ternary_layernorm_quantize(const void *X, int in_kind, const void *residual,
   const void *const same[6][2] = {{X, residual}};
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
   const LnArgs a = {X, residual, gain, beta, H, Y, mean, rstd, scale, Q, eps, R, C};
-  const RowPlan p = row_plan(R, C, in_kind, false);
+  const RowPlan p = ln_plan(R, C, in_kind);
   if (p.v) {
     row_launch<LnReg>(in_kind, p, a, stream);
     return done();

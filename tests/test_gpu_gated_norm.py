@@ -16,7 +16,7 @@ INF, NAN = float("inf"), float("nan")
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("R,C", ROWS + [(1100, 1280), (1024, 2000)])
+@pytest.mark.parametrize("R,C", ROWS + [(1100, 1280), (1024, 2000), (2500, 3120), (2100, 1301), (1100, 5000), (1030, 7001), (4200, 1540), (520, 6001)])
 def test_layernorm(R, C, kind):
     say(f"layernorm {R}x{C} {kind}")
     dt, g = KINDS[kind], gen("ln", R, C, kind)
