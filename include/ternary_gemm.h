@@ -402,7 +402,7 @@ int ternary_layernorm_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
  * Any K up to TGEMM_INT8_MAX_CONTRACTION (TGEMM_ERR_BOUND).  Its gradients: dX is
  * this call on dZ's int8 rows and the transposed weights, quantized row by row
  * like the weights; dW is ternary_gemm_s8_dw_scaled on both operands' columns.
- * N is at most 2^29 (TGEMM_ERR_DIM).
+ * N is at most 2^27 (TGEMM_ERR_DIM).
  * Workspace: where K is not a multiple of 16 or an operand's base not 16-byte
  * aligned, more than 64 rows need it (operands are copied into aligned rows).
  * The query takes the smallest alignment of A and W, in bytes.
@@ -427,7 +427,7 @@ int ternary_gemm_s8s8_workspace(int64_t M, int64_t N, int64_t K, int64_t align, 
  *   bias     float [2N], or NULL
  *   Y        [M][N] of out_kind
  *   Z        [M][2N] of out_kind, (g | u) for ternary_gated_backward, or NULL
- * The checks of ternary_gemm_s8_epilogue; N is at most 2^29 (TGEMM_ERR_DIM).
+ * The checks of ternary_gemm_s8_epilogue; N is at most 2^27 (TGEMM_ERR_DIM).
  * Workspace: more than 128 to 192 rows need one (the weights' codes are decoded
  * into it, 2 N K bytes), and so do fewer where K is not a multiple of 64 or A or
  * Wpacked not 16-byte aligned.  The query takes their smallest alignment, in bytes.

@@ -899,6 +899,7 @@ def ternary_gemm_s8_gated(A, Wpacked, a_row_scale, gate_scale, up_scale, bias=No
                                       _raw_stream(stream, dev)))
     return Y, Z
 
+
 def ternary_gated_backward(dY, Z, gate_scale, up_scale, act="silu", bias=True, dZ=None, dbias=None, Q=None, scale=None,
                            workspace=None, stream=None):
     """(dZ [R][2C], dbias float32 [2C], Q int8 [R][2C], scale float32 [R]) from

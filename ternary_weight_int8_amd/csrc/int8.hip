@@ -484,8 +484,8 @@ void tgemm_int8(MArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int cur = u & 1, nxt = U == 1 ? 0 : cur ^ 1;
-          const bool reads = u + 1 < U || !kLast;
-            v4i qn[FM], pn[FN];
+      const bool reads = u + 1 < U || !kLast;
+      v4i qn[FM], pn[FN];
       // chunks past the contraction: A's count as zeros
       if (kLast && a.tail != C::CH && 4 * u + (lane >> 4) >= a.tail) {
 #pragma unroll
@@ -567,7 +567,6 @@ void tgemm_int8(MArgs a) {
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
-
 
 // ---------------------------------------------------------------------------
 // Few rows (s8s8): the weights are nearly all of the bytes, and a workgroup of 8
@@ -718,24 +717,27 @@ void int8_few(FewArgs a) {
 // Rows laid out for tgemm_int8: as they are, with a length that is whole 16-byte
 // chunks (zeros past the contraction), or decoded from stored codes, a gate's row
 // and an up projection's in turn.  A workgroup takes eight rows, a thread 16 bytes
-// at a time, four loads ahead of their stores.
+// at a time, four loads ahead of their stores; past 2^20 groups it takes more of them
+// (a launch has fewer than 2^32 threads).
 // ---------------------------------------------------------------------------
 constexpr int kLayT = 256, kLayRows = 8;
+constexpr int64_t kLayGrid = 1 << 20;
 template <class Load>
 __device__ __forceinline__ void lay_out(int8_t *dst, int64_t R, int32_t chunks, Load load) {
-  const int64_t row0 = (int64_t)blockIdx.x * kLayRows;
-  const uint32_t rows = (uint32_t)(R - row0 < kLayRows ? R - row0 : kLayRows), n = rows * (uint32_t)chunks;
-  v4i *q = reinterpret_cast<v4i *>(dst) + row0 * chunks;
-  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += 4 * kLayT) {
-    v4i v[4];
+  for (int64_t row0 = (int64_t)blockIdx.x * kLayRows; row0 < R; row0 += (int64_t)gridDim.x * kLayRows) {
+    const uint32_t rows = (uint32_t)(R - row0 < kLayRows ? R - row0 : kLayRows), n = rows * (uint32_t)chunks;
+    v4i *q = reinterpret_cast<v4i *>(dst) + row0 * chunks;
+    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += 4 * kLayT) {
+      v4i v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t i = i0 + k * kLayT;
-      if (i < n) v[k] = load(row0 + i / (uint32_t)chunks, i % (uint32_t)chunks);
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t i = i0 + k * kLayT;
+        if (i < n) v[k] = load(row0 + i / (uint32_t)chunks, i % (uint32_t)chunks);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k * kLayT < n) q[i0 + k * kLayT] = v[k];
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i0 + k * kLayT < n) q[i0 + k * kLayT] = v[k];
   }
 }
 __global__ __launch_bounds__(kLayT) void lay_rows(const int8_t *__restrict__ src, int8_t *__restrict__ dst, int64_t R,
@@ -782,7 +784,9 @@ bool mul_ok(int64_t a, int64_t b, int64_t *out) {
   *out = a * b;
   return true;
 }
-constexpr int64_t kMaxCols = (int64_t)1 << 29;   // a tile's loads of biases reach 4 N bytes in 32 bits
+// few rows: 16 threads a column at most, fewer than 2^32 a launch; the tiles' loads of
+// biases reach 8 N bytes in 32 bits
+constexpr int64_t kMaxCols = (int64_t)1 << 27;
 int check_sizes(int64_t M, int64_t N, int64_t K) {
   int64_t t;
   if (M < 1 || N < 1 || K < 1) return TGEMM_ERR_DIM;
@@ -790,7 +794,7 @@ int check_sizes(int64_t M, int64_t N, int64_t K) {
   if (!mul_ok(M, K, &t) || !mul_ok(t, 8, &t) || !mul_ok(N, K, &t) || !mul_ok(t, 8, &t) || !mul_ok(M, N, &t) ||
       !mul_ok(t, 8, &t))
     return TGEMM_ERR_DIM;
-  if (N > kMaxCols || M / kLayRows > INT32_MAX - 1 || ceil_div(M, 16) * ceil_div(2 * N, 16) > INT32_MAX) return TGEMM_ERR_DIM;
+  if (N > kMaxCols || ceil_div(M, 16) * ceil_div(2 * N, 16) > INT32_MAX) return TGEMM_ERR_DIM;
   return TGEMM_OK;
 }
 
@@ -874,8 +878,12 @@ int pick_mm_act(const MArgs &a, const Machine &mc, hipStream_t stream) {
   return epi_of(a.o.act) == EPI_POLY ? pick_mm<EPI_POLY | FLAG>(a, mc, stream) : pick_mm<EPI_SIGM | FLAG>(a, mc, stream);
 }
 
+dim3 lay_grid(int64_t R) {
+  const int64_t n = ceil_div(R, kLayRows);
+  return dim3((unsigned)(n < kLayGrid ? n : kLayGrid));
+}
 void lay(const int8_t *src, int8_t *dst, int64_t R, int64_t K, int64_t Kp, hipStream_t stream) {
-  hipLaunchKernelGGL(lay_rows, dim3((unsigned)ceil_div(R, kLayRows)), dim3(kLayT), 0, stream, src, dst, R, K, (int32_t)(Kp / 16));
+  hipLaunchKernelGGL(lay_rows, lay_grid(R), dim3(kLayT), 0, stream, src, dst, R, K, (int32_t)(Kp / 16));
 }
 
 // Few rows go to int8_few, which needs no layout: 32, and up to 64 where the
@@ -1015,8 +1023,7 @@ int ternary_gemm_s8_gated(const int8_t *A, const uint8_t *Wpacked, const float *
                      stream);
   int8_t *la = static_cast<int8_t *>(workspace), *lw = la + l.a_bytes;
   if (l.a_bytes) lay(A, la, M, K, l.kp, stream);
-  hipLaunchKernelGGL(lay_gated, dim3((unsigned)ceil_div(2 * N, kLayRows)), dim3(kLayT), 0, stream, Wpacked, lw, N, K,
-                     (int32_t)(l.kp / 16));
+  hipLaunchKernelGGL(lay_gated, lay_grid(2 * N), dim3(kLayT), 0, stream, Wpacked, lw, N, K, (int32_t)(l.kp / 16));
   Out o{};
   o.ptr = Y;
   o.rs = a_row_scale;

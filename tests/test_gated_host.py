@@ -61,7 +61,7 @@ def test_product_checks(call):
         assert call(kind=kind) == B.ERR_KIND
     for act in (-1, 5):
         assert call(act=act) == B.ERR_VALUE
-    for M, N, K in ((0, 8, 16), (4, 0, 16), (4, 8, 0), (-4, 8, 16), (1 << 40, 1 << 40, 4), (4, (1 << 29) + 1, 4), (1 << 36, 8, 4)):
+    for M, N, K in ((0, 8, 16), (4, 0, 16), (4, 8, 0), (-4, 8, 16), (1 << 40, 1 << 40, 4), (4, (1 << 29) + 1, 4), (4, (1 << 27) + 1, 4), (1 << 36, 8, 4)):
         assert call(M=M, N=N, K=K) == B.ERR_DIM, (M, N, K)
     assert gated(K=18) == B.ERR_PACK and gated(K=16777220) == B.ERR_BOUND and s8s8(K=131072) == B.ERR_BOUND
 

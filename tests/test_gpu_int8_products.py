@@ -145,3 +145,46 @@ def test_offsets_past_32_bits():
     w, c = W8[-70:].contiguous(), cs[-70:].contiguous()
     assert torch.equal(Y[:, -70:], B.ternary_gemm_s8s8_epilogue(A, w, rs, c, out_dtype=torch.float32)[0])
     assert torch.equal(few, Y[:3])
+
+
+def test_very_many_rows_and_columns():
+    """More rows to lay out than a launch has workgroups for: 2^27 of the gated weights, then 2^27 + 5 of A."""
+    say("very many rows and columns")
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GiB")
+    g, N = gen("many"), 1 << 26
+    A, W, rs = int8(g, 1, 4), packed(g, 2 * N, 4), torch.ones(1, device=DEV)
+    Y, _ = B.ternary_gemm_s8_gated(A, W, rs, 0.5, 0.25, act="none", out_dtype=torch.float32)
+    acc = torch.zeros(2 * N, dtype=torch.int32, device=DEV)
+    for k in range(4):
+        c = (W[:, 0] >> (2 * k)) & 3
+        acc += ((c & 1).int() - (c >> 1).int()) * int(A[0, k])
+    assert torch.equal(Y[0], (acc[:N].float() * 0.5) * (acc[N:].float() * 0.25))
+    del Y, W, acc
+    M = (1 << 27) + 5
+    A, W, rs = int8(g, M, 17), int8(g, 3, 17), torch.rand(M, generator=g, device=DEV)
+    Y, _ = B.ternary_gemm_s8s8_epilogue(A, W, rs, out_dtype=torch.float32)
+    for n in range(3):
+        acc = torch.zeros(M, dtype=torch.int32, device=DEV)
+        for k in range(17):
+            acc += A[:, k].int() * int(W[n, k])
+        assert torch.equal(Y[:, n], acc.float() * rs)
+
+
+def test_longest_gated_contraction():
+    """16777212 products a sum: a tile's rows lie up to 2^32 bytes apart, and the last of the sums is as large as it can be."""
+    say("longest gated contraction")
+    M, N, K, part = 300, 2, 16777212, 1 << 18
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB")
+    g = gen("long gated")
+    A, W, rs = int8(g, M, K), packed(g, 2 * N, K), torch.ones(M, device=DEV)
+    A[M - 1], W[0] = 127, 0x55                        # the gate's first row: every weight 1
+    _, Z = B.ternary_gemm_s8_gated(A, W, rs, 1.0, 1.0, act="none", out_dtype=torch.float32, save=True)
+    want = torch.zeros(M, 2 * N, dtype=torch.float64, device=DEV)
+    for b in range(0, K // 4, part):
+        codes = torch.stack([(W[:, b:b + part] >> (2 * k)) & 3 for k in range(4)], dim=2).flatten(1)
+        w = (codes & 1).double() - (codes >> 1).double()
+        want += A[:, 4 * b:4 * (b + part)].double() @ w.t().contiguous()
+    assert want[M - 1, 0] == 127 * K
+    assert torch.equal(Z, want.float())               # whole numbers: exact in 64 bits, rounded once
