@@ -790,7 +790,7 @@ __global__ __launch_bounds__(kNT) void col_sums(const T *__restrict__ A, const T
 // left (from the registers: the row is still read once), so that a mean far
 // larger than the deviation loses nothing to cancellation.  Bound by HBM: 16384x1280
 // bf16 with residual and Y, 189 MB, 34 us (the RMS norm 33), 16384x3456 float32, 963 MB,
-// 204 us.  Column sums of both kinds (dgain, dbeta) cost the backward pass little more
+// 188 us.  Column sums of both kinds (dgain, dbeta) cost the backward pass little more
 // than one: 16384x3456 bf16 91 us against 84, 16384x1280 float32 62 against 60.
 // ---------------------------------------------------------------------------
 struct LnArgs {

@@ -202,3 +202,21 @@ def test_offsets_past_32_bits():
     want = B.ternary_gated_backward(dY[-3:].contiguous(), Z[-3:].contiguous(), 1.0, 1.0, bias=False)
     assert torch.equal(dZ[-3:], want[0]) and torch.equal(Q[-3:], want[2]) and torch.equal(s[-3:], want[3])
     assert not bool(dZ[:-3].any())
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """A call launches on the current device: tensors of another one are an error before any launch."""
+    say("another current device")
+    x, q, w = (torch.ones(2, 64, device=DEV, dtype=d) for d in (torch.float32, torch.int8, torch.uint8))
+    v, z = torch.ones(64, device=DEV), torch.ones(2, 128, device=DEV)
+    r = torch.ones(2, device=DEV)
+    calls = (lambda: B.ternary_layernorm_quantize(x, v), lambda: B.ternary_layernorm_backward(x, x, v, r, r),
+             lambda: B.ternary_gated_backward(x, z, 1.0, 1.0), lambda: B.ternary_gemm_s8s8_epilogue(q, q, r),
+             lambda: B.ternary_gemm_s8_gated(q, w[:, :16].contiguous(), r, 1.0, 1.0))
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: x.device.index + 1)
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
