@@ -52,12 +52,14 @@ PREP_KERNELS = ("pack", "quantize_rows", "quantize_cols")
 
 
 def source_digest(kernel=None):
-    """sha256 of the source file that holds a kernel (the GEMM kernels'
-    file unless the kernel is one of the packer / quantizer's)."""
-    name = "prep.hip" if kernel in PREP_KERNELS else "ternary_gemm.hip"
-    src = os.path.join(ROOT, "ternary_weight_int8_amd", "csrc", name)
-    with open(src, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()
+    """sha256 of the source files that hold a kernel (the GEMM kernels' file
+    and the header that it shares with the other products, unless the kernel is
+    one of the packer / quantizer's)."""
+    h = hashlib.sha256()
+    for name in ("prep.hip",) if kernel in PREP_KERNELS else ("ternary_gemm.hip", "product.h"):
+        with open(os.path.join(ROOT, "ternary_weight_int8_amd", "csrc", name), "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
 
 
 def recorded_traffic(kernel, workload_tag):
