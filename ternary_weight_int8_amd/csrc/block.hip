@@ -18,6 +18,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 #include <vector>
 
 #include "checks.h"
@@ -59,7 +60,8 @@ __device__ __forceinline__ int8_t quant1(float y, float s) {
 
 // sum and maximum over the workgroup's four waves; `part` has 4 entries and
 // is free again when every thread has passed the next barrier
-__device__ __forceinline__ float block_sum(float v, float *part) {
+template <class F>
+__device__ __forceinline__ F block_sum(F v, F *part) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
   __syncthreads();
@@ -156,6 +158,24 @@ __device__ __forceinline__ float wave_sum(float v) {
   v += __uint_as_float(dpp<kMirror>(__float_as_uint(v)));
   return (lane_f(v, 0) + lane_f(v, 16)) + (lane_f(v, 32) + lane_f(v, 48));
 }
+// the same in 64 bits
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32 | dpp<CTRL>((uint32_t)b));
+}
+__device__ __forceinline__ double lane_f(double v, int l) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(b >> 32), l), lo = __builtin_amdgcn_readlane((int)b, l);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  v += dpp<kHalfMirror>(v);
+  v += dpp<kMirror>(v);
+  return (lane_f(v, 0) + lane_f(v, 16)) + (lane_f(v, 32) + lane_f(v, 48));
+}
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = umax(v, dpp<kXor1>(v));
@@ -182,6 +202,21 @@ __device__ __forceinline__ float row_sum(float v, float *part) {
     v += __uint_as_float(dpp<kXor2>(__float_as_uint(v)));
     v += __uint_as_float(dpp<kHalfMirror>(__float_as_uint(v)));
     v += __uint_as_float(dpp<kMirror>(__float_as_uint(v)));
+  }
+  return v;
+}
+// the waves' sums in 64 bits, v the same in every lane of a wave
+template <int W>
+__device__ __forceinline__ double row_sum_waves(double v, double *part) {
+  if constexpr (W == 0) {
+    const int lane = threadIdx.x & 63, l = lane & 15;
+    if (lane == 0) part[threadIdx.x >> 6] = v;
+    lds_barrier();
+    v = l < (int)(blockDim.x >> 6) ? part[l] : 0.;
+    v += dpp<kXor1>(v);
+    v += dpp<kXor2>(v);
+    v += dpp<kHalfMirror>(v);
+    v += dpp<kMirror>(v);
   }
   return v;
 }
@@ -787,8 +822,14 @@ __global__ __launch_bounds__(kNT) void col_sums(const T *__restrict__ A, const T
 // ---------------------------------------------------------------------------
 // Layer norm.  As the RMS norm, with the mean taken off first: the mean from one
 // sum over the row, the variance from a second one over the squares of what is
-// left (from the registers: the row is still read once), so that a mean far
-// larger than the deviation loses nothing to cancellation.  Bound by HBM: 16384x1280
+// left (from the registers: the row is still read once).  A mean far above the
+// deviation has to cost neither of them anything.  bfloat16 values of one size add up
+// exactly in float32 (8 bits each, at most 2^14 of them), and the mean's rounding is
+// 2^-16 of their spacing.  float32 values do not: 1280 of them about 4096 that deviate by
+// 0.03 leave a float32 mean off by up to 2% of the deviation, so their sum and the mean
+// are held to more bits (Mean), at 3% of the time of 16384x3456 without a residual and
+// nothing with one.  A row of one value leaves exact zeros either way.
+// Bound by HBM: 16384x1280
 // bf16 with residual and Y, 189 MB, 34 us (the RMS norm 33), 16384x3456 float32, 963 MB,
 // 188 us.  Column sums of both kinds (dgain, dbeta) cost the backward pass little more
 // than one: 16384x3456 bf16 91 us against 84, 16384x1280 float32 62 against 60.
@@ -801,53 +842,71 @@ struct LnArgs {
   int8_t *Q;
   float eps;
   int64_t R, C;
+  double n, inv;   // C and 1 / C
 };
 
-__device__ __forceinline__ float ln_y(float d, float rstd, float gain, float beta) {
-  return __builtin_fmaf(d * rstd, gain, beta);
+// The mean of C values from their sum in 64 bits: hi is its nearest float32, lo the
+// rest (sum - C hi is exact by fma, and 0 where hi is the mean).  With d = h - hi,
+//     sum (h - mean)^2 / C = sum d^2 / C - lo^2,  (h - mean) rstd = d rstd - lo rstd
+// No h, itself a float32, is nearer to the mean than hi, so lo^2 is at most half of
+// sum d^2 / C and the difference loses one bit.
+struct Mean {
+  float hi, lo;
+};
+__device__ __forceinline__ Mean mean_of(double sum, double C, double invC) {
+  const float hi = (float)(sum * invC);
+  return {hi, (float)(__builtin_fma(-C, (double)hi, sum) * invC)};
+}
+__device__ __forceinline__ float ln_rstd(float ss, const Mean &m, float C, float eps) {
+  return __fdiv_rn(1.f, __fsqrt_rn(__builtin_fmaf(-m.lo, m.lo, __fdiv_rn(ss, C)) + eps));
+}
+// shift: -lo rstd
+__device__ __forceinline__ float ln_y(float d, float rstd, float shift, float gain, float beta) {
+  return __builtin_fmaf(__builtin_fmaf(d, rstd, shift), gain, beta);
 }
 
 template <class T>
 __global__ __launch_bounds__(kNT) void ln_rows(LnArgs a) {
-  __shared__ float part[4];
+  __shared__ double part[4];
+  __shared__ float part2[4];
   __shared__ uint32_t upart[4];
   const int t = threadIdx.x;
   for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {
     const T *x = static_cast<const T *>(a.X) + row * a.C;
     const T *res = a.res ? static_cast<const T *>(a.res) + row * a.C : nullptr;
     T *h = res ? static_cast<T *>(a.H) + row * a.C : nullptr;
-    float sum = 0.f;
+    double sum = 0.;
     for (int64_t c = t; c < a.C; c += kNT) {
       T v = x[c];
       if (res) {
         v = narrow<T>(widen(v) + widen(res[c]));
         h[c] = v;
       }
-      sum += widen(v);
+      sum += (double)widen(v);
     }
-    const float mean = __fdiv_rn(block_sum(sum, part), (float)a.C);
+    const Mean mean = mean_of(block_sum(sum, part), a.n, a.inv);
     const T *src = res ? h : x;
     float ss = 0.f;
     for (int64_t c = t; c < a.C; c += kNT) {
-      const float d = widen(src[c]) - mean;
+      const float d = widen(src[c]) - mean.hi;
       ss = __builtin_fmaf(d, d, ss);
     }
-    const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(block_sum(ss, part), (float)a.C) + a.eps));
+    const float rstd = ln_rstd(block_sum(ss, part2), mean, (float)a.C, a.eps), shift = -mean.lo * rstd;
     uint32_t m = 0;
     for (int64_t c = t; c < a.C; c += kNT)
-      m = umax(m, mag(ln_y(widen(src[c]) - mean, rstd, a.gain[c], a.beta ? a.beta[c] : 0.f)));
+      m = umax(m, mag(ln_y(widen(src[c]) - mean.hi, rstd, shift, a.gain[c], a.beta ? a.beta[c] : 0.f)));
     const float s = __fdiv_rn(block_max(m, upart), 127.f);
     if (t == 0) {
       a.scale[row] = s;
       if (a.rstd) {
-        a.mean[row] = mean;
+        a.mean[row] = mean.hi;
         a.rstd[row] = rstd;
       }
     }
     int8_t *q = a.Q + row * a.C;
     T *y = a.Y ? static_cast<T *>(a.Y) + row * a.C : nullptr;
     for (int64_t c = t; c < a.C; c += kNT) {
-      const float v = ln_y(widen(src[c]) - mean, rstd, a.gain[c], a.beta ? a.beta[c] : 0.f);
+      const float v = ln_y(widen(src[c]) - mean.hi, rstd, shift, a.gain[c], a.beta ? a.beta[c] : 0.f);
       if (y) y[c] = narrow<T>(v);
       q[c] = quant1(v, s);
     }
@@ -861,7 +920,9 @@ __global__ __launch_bounds__(max_t(W, V)) void ln_reg(LnArgs a) {
   // (16384x3456 at one unit a lane, residual 177 -> 149 us, without 139 -> 131; four units spill).
   // bfloat16 rows gain nothing from it without a residual and lose with one (89 -> 97 us).
   constexpr bool kAhead = W == 0 && U == 4 && V <= 3;
-  __shared__ float part[2][16], part2[2][16];
+  constexpr bool kSplit = U == 4;   // the mean in two parts
+  __shared__ std::conditional_t<kSplit, double, float> part[2][16];
+  __shared__ float part2[2][16];
   __shared__ uint32_t upart[2][16];
   const int t = W ? threadIdx.x & 63 : threadIdx.x;
   const int grp = W ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
@@ -877,6 +938,9 @@ __global__ __launch_bounds__(max_t(W, V)) void ln_reg(LnArgs a) {
       if (a.beta) load_f<U>(a.beta + un.off[j], beta[j]);
     }
   }
+  // kSplit: the lane's elements (0 in lanes past the row), one over lane 0's, and the wave's
+  const float own = (float)(U * un.n - (un.last >= 0 ? un.dup : 0)), per = __fdiv_rn(1.f, fmaxf(own, 1.f));
+  const double wave_own = (double)wave_sum(own);
   int flip = 0;
   const int groups = W ? (int)(blockDim.x >> 6) : 1;
   const int64_t stride = (int64_t)gridDim.x * groups;
@@ -924,16 +988,48 @@ __global__ __launch_bounds__(max_t(W, V)) void ln_reg(LnArgs a) {
           h[j] = pack(f);
         }
     }
-    float sum = 0.f;
+    Mean mean;
+    if constexpr (kSplit) {
+      // A lane's sum in float32 is of differences from its first value, a wave's of
+      // differences from the mean of its lane 0: both are of the size of the deviation.
+      float first = 0.f, diff = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (un.on(j)) {
-        float f[U];
-        unpack(h[j], f);
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) {
+          float f[U];
+          unpack(h[j], f);
+          if (j == 0) first = f[0];
 #pragma unroll
-        for (int i = 0; i < U; ++i) sum += j == un.last && i < un.dup ? 0.f : f[i];
+          for (int i = 0; i < U; ++i) diff += j == un.last && i < un.dup ? 0.f : f[i] - first;
+        }
+      const float about = lane_f(__builtin_fmaf(diff, per, first), 0);
+      const float rest = wave_sum(__builtin_fmaf(own, first - about, diff));
+      double sum = __builtin_fma(wave_own, (double)about, (double)rest);
+      if (!(fabsf(rest) < __builtin_inff())) {   // the differences pass float32, or a value is not finite
+        sum = 0.;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (un.on(j)) {
+            float f[U];
+            unpack(h[j], f);
+#pragma unroll
+            for (int i = 0; i < U; ++i) sum += (double)(j == un.last && i < un.dup ? 0.f : f[i]);
+          }
+        sum = wave_sum(sum);
       }
-    const float mean = __fdiv_rn(row_sum<W>(sum, part[flip]), (float)a.C);
+      mean = mean_of(row_sum_waves<W>(sum, part[flip]), a.n, a.inv);
+    } else {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (un.on(j)) {
+          float f[U];
+          unpack(h[j], f);
+#pragma unroll
+          for (int i = 0; i < U; ++i) sum += j == un.last && i < un.dup ? 0.f : f[i];
+        }
+      mean = {__fdiv_rn(row_sum<W>(sum, part[flip]), (float)a.C), 0.f};
+    }
     float y[V][U], ss = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -941,13 +1037,13 @@ __global__ __launch_bounds__(max_t(W, V)) void ln_reg(LnArgs a) {
         unpack(h[j], y[j]);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          y[j][i] -= mean;
+          y[j][i] -= mean.hi;
           const float d = j == un.last && i < un.dup ? 0.f : y[j][i];
           ss = __builtin_fmaf(d, d, ss);
         }
       }
     ss = row_sum<W>(ss, part2[flip]);
-    const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ss, (float)a.C) + a.eps));
+    const float rstd = ln_rstd(ss, mean, (float)a.C, a.eps), shift = kSplit ? -mean.lo * rstd : 0.f;
     if (a.res) {
       T *H = static_cast<T *>(a.H) + base;
 #pragma unroll
@@ -960,7 +1056,7 @@ __global__ __launch_bounds__(max_t(W, V)) void ln_reg(LnArgs a) {
       if (un.on(j)) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          y[j][i] = ln_y(y[j][i], rstd, gain[j][i], beta[j][i]);
+          y[j][i] = ln_y(y[j][i], rstd, shift, gain[j][i], beta[j][i]);
           m = umax(m, mag(y[j][i]));
         }
       }
@@ -969,7 +1065,7 @@ __global__ __launch_bounds__(max_t(W, V)) void ln_reg(LnArgs a) {
     if (t == 0) {
       a.scale[row] = s;
       if (a.rstd) {
-        a.mean[row] = mean;
+        a.mean[row] = mean.hi;
         a.rstd[row] = rstd;
       }
     }
@@ -1902,7 +1998,7 @@ int ternary_layernorm_quantize(const void *X, int in_kind, const void *residual,
   const Buf ins[] = {{X, xb}, {residual, xb}, {gain, 4 * C}, {beta, 4 * C}};
   const void *const same[6][2] = {{X, residual}};
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
-  const LnArgs a = {X, residual, gain, beta, H, Y, mean, rstd, scale, Q, eps, R, C};
+  const LnArgs a = {X, residual, gain, beta, H, Y, mean, rstd, scale, Q, eps, R, C, (double)C, 1. / (double)C};
   const RowPlan p = ln_plan(R, C, in_kind);
   if (p.v) {
     row_launch<LnReg>(in_kind, p, a, stream);
