@@ -803,12 +803,21 @@ __global__ __launch_bounds__(kNT) void epi_bwd_rows(EpiBwdArgs a) {
 
 // Partial column sums: workgroup (x, y) takes 256 columns, one a thread, and
 // the y-th strip of rows, and writes its sums to row y of P.  NORM: the terms
-// are dy * h * rstd; otherwise dy * act'(z).
+// are dy * h * rstd; otherwise dy * act'(z).  c0: the launch's first column (a launch
+// has fewer than 2^32 threads: launch_columns).
+constexpr int64_t kMaxColGrid = 1 << 20;
+template <class Launch>
+void launch_columns(int64_t C, int64_t each, Launch launch) {   // `each` columns a workgroup
+  for (int64_t c0 = 0; c0 < C; c0 += kMaxColGrid * each) {
+    const int64_t n = ceil_div(C - c0, each);
+    launch((unsigned)(n < kMaxColGrid ? n : kMaxColGrid), c0);
+  }
+}
 template <class T, bool NORM>
 __global__ __launch_bounds__(kNT) void col_sums(const T *__restrict__ A, const T *__restrict__ B,
                                                 const float *__restrict__ rstd, int32_t act, float *__restrict__ P,
-                                                int64_t R, int64_t C, int64_t strip) {
-  const int64_t c = (int64_t)blockIdx.x * kNT + threadIdx.x;
+                                                int64_t R, int64_t C, int64_t strip, int64_t c0) {
+  const int64_t c = c0 + (int64_t)blockIdx.x * kNT + threadIdx.x;
   if (c >= C) return;
   const int64_t r0 = (int64_t)blockIdx.y * strip, r1 = r0 + strip < R ? r0 + strip : R;
   float sum = 0.f;
@@ -1398,10 +1407,11 @@ struct Cols2Args {
   int64_t pitch;               // 2 C, or C for the first sums alone
   int64_t R, C, strip;
   int32_t act;                 // gated
+  int64_t c0;                  // the launch's first column
 };
 template <class T, bool NORM>
 __global__ __launch_bounds__(kNT) void col_sums2(Cols2Args k) {
-  const int64_t c = (int64_t)blockIdx.x * kNT + threadIdx.x;
+  const int64_t c = k.c0 + (int64_t)blockIdx.x * kNT + threadIdx.x;
   if (c >= k.C) return;
   const T *A = static_cast<const T *>(k.A), *B = static_cast<const T *>(k.B);
   const int64_t r0 = (int64_t)blockIdx.y * k.strip, r1 = r0 + k.strip < k.R ? r0 + k.strip : k.R;
@@ -1428,10 +1438,11 @@ __global__ __launch_bounds__(kNT) void col_sums2(Cols2Args k) {
 constexpr int kFinCols = 32, kFinGroups = 32, kFinT = kFinCols * kFinGroups;
 // (columns from `split` on go to out2: the sums of two operands side by side)
 __global__ __launch_bounds__(kFinT) void col_finish(const float *__restrict__ P, float *__restrict__ out,
-                                                    float *__restrict__ out2, int64_t split, int64_t rows, int64_t C) {
+                                                    float *__restrict__ out2, int64_t split, int64_t rows, int64_t C,
+                                                    int64_t c0) {
   __shared__ float part[kFinGroups][kFinCols + 1];
   const int c = threadIdx.x % kFinCols, g = threadIdx.x / kFinCols;
-  const int64_t col = (int64_t)blockIdx.x * kFinCols + c;
+  const int64_t col = c0 + (int64_t)blockIdx.x * kFinCols + c;
   float sum = 0.f;
   if (col < C)
     for (int64_t r0 = g; r0 < rows; r0 += 8 * kFinGroups) {
@@ -1660,13 +1671,16 @@ int done() { return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP; 
 
 
 void launch_finish(const float *P, float *out, int64_t rows, int64_t C, hipStream_t stream) {
-  hipLaunchKernelGGL(col_finish, dim3((unsigned)ceil_div(C, kFinCols)), dim3(kFinT), 0, stream, P, out, nullptr, C,
-                     rows, C);
+  launch_columns(C, kFinCols, [&](unsigned grid, int64_t c0) {
+    hipLaunchKernelGGL(col_finish, dim3(grid), dim3(kFinT), 0, stream, P, out, nullptr, C, rows, C, c0);
+  });
 }
 // rows of two sums side by side, C columns each (out2 null: of the first alone)
 void launch_finish2(const float *P, float *out, float *out2, int64_t rows, int64_t C, hipStream_t stream) {
   const int64_t n = out2 ? 2 * C : C;
-  hipLaunchKernelGGL(col_finish, dim3((unsigned)ceil_div(n, kFinCols)), dim3(kFinT), 0, stream, P, out, out2, C, rows, n);
+  launch_columns(n, kFinCols, [&](unsigned grid, int64_t c0) {
+    hipLaunchKernelGGL(col_finish, dim3(grid), dim3(kFinT), 0, stream, P, out, out2, C, rows, n, c0);
+  });
 }
 
 // W and V of the register kernels, for rows of U to 16384 elements: a wave a
@@ -1845,9 +1859,10 @@ template <class T, bool NORM>
 void launch_cols(const T *A, const T *B, const float *rstd, int act, float *P, float *out, int64_t R, int64_t C,
                  hipStream_t stream) {
   const int64_t strip = ceil_div(R, strips_of(R)), strips = ceil_div(R, strip);
-  const unsigned gx = (unsigned)ceil_div(C, kNT);
-  hipLaunchKernelGGL((col_sums<T, NORM>), dim3(gx, (unsigned)strips), dim3(kNT), 0, stream, A, B, rstd, act, P, R, C,
-                     strip);
+  launch_columns(C, kNT, [&](unsigned grid, int64_t c0) {
+    hipLaunchKernelGGL((col_sums<T, NORM>), dim3(grid, (unsigned)strips), dim3(kNT), 0, stream, A, B, rstd, act, P, R, C,
+                       strip, c0);
+  });
   launch_finish(P, out, strips, C, stream);
 }
 
@@ -1856,7 +1871,10 @@ void launch_cols2(Cols2Args k, float *out, float *out2, hipStream_t stream) {
   k.pitch = out2 ? 2 * k.C : k.C;
   k.strip = ceil_div(k.R, strips_of(k.R));
   const int64_t strips = ceil_div(k.R, k.strip);
-  hipLaunchKernelGGL((col_sums2<T, NORM>), dim3((unsigned)ceil_div(k.C, kNT), (unsigned)strips), dim3(kNT), 0, stream, k);
+  launch_columns(k.C, kNT, [&](unsigned grid, int64_t c0) {
+    k.c0 = c0;
+    hipLaunchKernelGGL((col_sums2<T, NORM>), dim3(grid, (unsigned)strips), dim3(kNT), 0, stream, k);
+  });
   launch_finish2(k.P, out, out2, strips, k.C, stream);
 }
 template <bool NORM>
@@ -2051,7 +2069,7 @@ int ternary_layernorm_backward(const void *dY, const void *H, int in_kind, const
     hipLaunchKernelGGL(ln_bwd_rows<float>, g, dim3(kNT), 0, stream, a);
   else
     hipLaunchKernelGGL(ln_bwd_rows<uint16_t>, g, dim3(kNT), 0, stream, a);
-  launch_cols2<true>(in_kind, {dY, H, mean, rstd, P, 0, R, C, 0, 0}, dgain, dbeta, stream);
+  launch_cols2<true>(in_kind, {dY, H, mean, rstd, P, 0, R, C, 0, 0, 0}, dgain, dbeta, stream);
   return done();
 }
 
@@ -2102,7 +2120,7 @@ int ternary_gated_backward(const void *dY, const void *Z, int in_kind, int act, 
     hipLaunchKernelGGL(gated_bwd_rows<float>, g, dim3(kNT), 0, stream, a);
   else
     hipLaunchKernelGGL(gated_bwd_rows<uint16_t>, g, dim3(kNT), 0, stream, a);
-  if (dbias) launch_cols2<false>(in_kind, {dY, Z, nullptr, nullptr, P, 0, R, C, 0, act}, dbias, dbias + C, stream);
+  if (dbias) launch_cols2<false>(in_kind, {dY, Z, nullptr, nullptr, P, 0, R, C, 0, act, 0}, dbias, dbias + C, stream);
   return done();
 }
 
