@@ -1703,7 +1703,7 @@ struct RowPlan {
   int w, v, bt;
   int64_t grid;   // workgroups
 };
-RowPlan row_plan(int64_t R, int64_t C, int kind, bool sums) {
+RowPlan row_plan(int64_t R, int64_t C, int kind, bool sums, bool one_ok = true) {
   const int U = kind == TGEMM_IN_F32 ? kU<float> : kU<uint16_t>;
   RowPlan p = {0, 0, 0, 0};
   const int64_t nu = ceil_div(C, U);
@@ -1711,7 +1711,7 @@ RowPlan row_plan(int64_t R, int64_t C, int kind, bool sums) {
   p.w = nu <= 64 || (nu <= 256 && R >= 1024 && !sums) ? 1 : 0;
   p.v = (int)ceil_div(nu, p.w ? 64 : 1024);
   p.bt = p.w ? 256 : 64 * (int)ceil_div(nu, 64 * p.v);
-  const bool one = sums && nu <= 64 && R <= 32;
+  const bool one = one_ok && sums && nu <= 64 && R <= 32;
   if (one) p.bt = 64 * (int)(R < 16 ? R : 16);
   const int64_t groups = ceil_div(R, p.w ? p.bt / 64 : 1), per_cu = 64 * (sums ? kBwdWaves : kNormWaves) / p.bt;
   int64_t cap = kCUs * (per_cu > 1 ? per_cu : 1);
@@ -1809,7 +1809,9 @@ void row_launch(int kind, const RowPlan &p, const typename Kernel::Args &a, hipS
 // pass has several times the instructions, and one CU for all of them: past two units
 // a lane in float32 and one in bfloat16 it is so up to 16 rows, where the GPU takes as
 // long as the host (16x729 f32 12.8 us a call against 17.0, 12.4 against 5.9 in a graph;
-// 27 rows 14.9 and 15.2, 32 rows 17.3 and 17.6).
+// 27 rows 14.9 and 15.2, 32 rows 17.3 and 17.6).  Without dbias there is no second
+// launch and no workspace to save, and a few rows are as many workgroups' (in a graph,
+// 16x729 f32 3.2 us against 9.8, 32x500 bf16 3.3 against 7.6).
 bool one_ok(int64_t R, int64_t C, int kind, bool gated) {
   const bool f32 = kind == TGEMM_IN_F32;
   const int64_t U = f32 ? kU<float> : kU<uint16_t>, units = ceil_div(C, U);
@@ -2098,7 +2100,7 @@ int ternary_gated_backward(const void *dY, const void *Z, int in_kind, int act, 
   if (alias(outs, ins, same)) return TGEMM_ERR_ALIAS;
   float *P = static_cast<float *>(workspace);
   GatedBwdArgs a = {dY, Z, dZ, Q, scale, dbias ? P : nullptr, gate_scale, up_scale, R, C, act};
-  if (one_ok(R, C, in_kind, true)) {
+  if (dbias && one_ok(R, C, in_kind, true)) {
     a.P = dbias;
     if (is_sigm(act))
       one_launch<GatedBwdSigmOne>(in_kind, R, C, a, stream);
@@ -2106,7 +2108,7 @@ int ternary_gated_backward(const void *dY, const void *Z, int in_kind, int act, 
       one_launch<GatedBwdPolyOne>(in_kind, R, C, a, stream);
     return done();
   }
-  const RowPlan p = row_plan(R, C, in_kind, true);
+  const RowPlan p = row_plan(R, C, in_kind, true, dbias != nullptr);
   if (p.v) {
     if (is_sigm(act))
       row_launch<GatedBwdSigm>(in_kind, p, a, stream);
