@@ -518,6 +518,15 @@ const char *ternary_gemm_status_str(int status);
                                   8-wave workgroup per 128 x 128 output tile,
                                   operands loaded straight into LDS          */
 
+#define TGEMM_KERNEL_INT8 6    /* the gated product and the product with int8
+                                  weights: persistent workgroups over output
+                                  tiles of one of six sizes, operands loaded
+                                  straight into LDS                           */
+#define TGEMM_KERNEL_INT8_FEW 7 /* the product with int8 weights of few rows:
+                                  one 8- or 16-wave workgroup per 16, 32 or 64
+                                  output columns and 16 or 32 rows, its waves
+                                  splitting the contraction                   */
+
 typedef struct tgemm_plan {
     int64_t out_rows, out_cols, contraction;
     int32_t tile_rows, tile_cols;
@@ -553,6 +562,20 @@ int ternary_gemm_machine(int32_t *cus, int32_t *xcds);
  */
 int ternary_gemm_epilogue_plan(int64_t M, int64_t N, int64_t K, int64_t align, int32_t cus, int32_t xcds,
                                tgemm_plan *plan);
+
+/*
+ * The plans of ternary_gemm_s8s8_epilogue and ternary_gemm_s8_gated with these
+ * arguments (align: the smallest alignment of the operands, in bytes; residual and
+ * save: whether there is a residual and a Z): TGEMM_KERNEL_INT8_FEW or
+ * TGEMM_KERNEL_INT8, and TGEMM_KERNEL_SKINNY (blocks of up to 32 rows) or
+ * TGEMM_KERNEL_INT8.  The gated product's plan counts the product's columns, 2 N of
+ * them.  fast_path: the operands' rows are read where they are (the gated product's
+ * weights are decoded into the workspace by every call with TGEMM_KERNEL_INT8).
+ */
+int ternary_gemm_s8s8_plan(int64_t M, int64_t N, int64_t K, int64_t align, int act, int residual, int save, int out_kind,
+                           int32_t cus, int32_t xcds, tgemm_plan *plan);
+int ternary_gemm_s8_gated_plan(int64_t M, int64_t N, int64_t K, int64_t align, int act, int save, int out_kind, int32_t cus,
+                               int32_t xcds, tgemm_plan *plan);
 
 /*
  * Output tile that workgroup `workgroup` computes in its iteration

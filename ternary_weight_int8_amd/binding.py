@@ -60,6 +60,8 @@ EXPORTS = (
     "ternary_gemm_s8s8_workspace",
     "ternary_gemm_s8_gated",
     "ternary_gemm_s8_gated_workspace",
+    "ternary_gemm_s8s8_plan",
+    "ternary_gemm_s8_gated_plan",
 )
 
 OPS = {"fwd": 0, "dx": 1, "dw": 2}
@@ -80,6 +82,7 @@ class TgemmPlan(ctypes.Structure):
 
 
 KERNEL_TILED, KERNEL_SPLIT, KERNEL_STREAM, KERNEL_SKINNY, KERNEL_RING = 0, 2, 3, 4, 5   # TgemmPlan.kernel
+KERNEL_INT8, KERNEL_INT8_FEW = 6, 7
 
 
 class TernaryGemmError(RuntimeError):
@@ -156,7 +159,9 @@ def lib():
                 ("ternary_gemm_s8s8_epilogue", [p, p, p, p, p, i32, p, p, p, i32, i64, i64, i64, p, i64, p]),
                 ("ternary_gemm_s8s8_workspace", [i64, i64, i64, i64, pi64]),
                 ("ternary_gemm_s8_gated", [p, p, p, f32, f32, p, i32, p, p, i32, i64, i64, i64, p, i64, p]),
-                ("ternary_gemm_s8_gated_workspace", [i64, i64, i64, i64, pi64])):
+                ("ternary_gemm_s8_gated_workspace", [i64, i64, i64, i64, pi64]),
+                ("ternary_gemm_s8s8_plan", [i64, i64, i64, i64, i32, i32, i32, i32, i32, i32, ctypes.POINTER(TgemmPlan)]),
+                ("ternary_gemm_s8_gated_plan", [i64, i64, i64, i64, i32, i32, i32, i32, i32, ctypes.POINTER(TgemmPlan)])):
             f = getattr(L, name)
             f.argtypes = args
             f.restype = ctypes.c_int
@@ -215,6 +220,24 @@ def epilogue_plan(M: int, N: int, K: int, align: int = 256, cus: int = 256, xcds
     pl = TgemmPlan()
     _done("ternary_gemm_epilogue_plan",
           lib().ternary_gemm_epilogue_plan(M, N, K, align, cus, xcds, ctypes.byref(pl)))
+    return pl
+
+
+def s8s8_plan(M: int, N: int, K: int, align: int = 256, act: str = "none", residual: bool = False, save: bool = False,
+              kind: int = OUT_BF16, cus: int = 256, xcds: int = 8):
+    """The launch plan of ternary_gemm_s8s8_epilogue, for MI355X unless cus and xcds name another machine."""
+    pl = TgemmPlan()
+    _done("ternary_gemm_s8s8_plan",
+          lib().ternary_gemm_s8s8_plan(M, N, K, align, _act(act), residual, save, kind, cus, xcds, ctypes.byref(pl)))
+    return pl
+
+
+def gated_plan(M: int, N: int, K: int, align: int = 256, act: str = "silu", save: bool = False, kind: int = OUT_BF16,
+               cus: int = 256, xcds: int = 8):
+    """The launch plan of ternary_gemm_s8_gated, for MI355X unless cus and xcds name another machine."""
+    pl = TgemmPlan()
+    _done("ternary_gemm_s8_gated_plan",
+          lib().ternary_gemm_s8_gated_plan(M, N, K, align, _act(act), save, kind, cus, xcds, ctypes.byref(pl)))
     return pl
 
 

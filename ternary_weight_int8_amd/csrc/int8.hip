@@ -804,19 +804,26 @@ typedef mm::Cfg<128, 192, 4, 2, 128, 3, 1> T128x192;
 typedef mm::Cfg<128, 128, 2, 4, 128, 4, 1> T128x128;
 typedef mm::Cfg<64, 128, 2, 2, 128, 3, 2> T64x128;
 typedef mm::Cfg<64, 64, 2, 2, 128, 4, 2> T64x64;
+constexpr int kStep = 128;   // of each of them
+static_assert(T256x192::KS == kStep && T256x128::KS == kStep && T128x192::KS == kStep && T128x128::KS == kStep &&
+                  T64x128::KS == kStep && T64x64::KS == kStep,
+              "time_of");
 
+int64_t mm_grid(int64_t tiles, int64_t percu, const Machine &mc) {
+  return tiles < mc.cus * percu ? round_up(tiles, mc.xcds) : mc.cus * percu;
+}
+// an XCD's tiles in flight, 8 columns wide: 16384x6912x1280 141 us, 16 wide 147, 4 144, 2 150
+int32_t mm_band(int32_t tiles_c) { return tiles_c < 8 ? tiles_c : 8; }
 template <class C, int E>
 int launch_mm(MArgs a, const Machine &mc, hipStream_t stream) {
   a.tiles_r = (int32_t)ceil_div(a.R, C::BM);
   a.tiles_c = (int32_t)ceil_div(a.Cc, C::BN);
   a.tiles = a.tiles_r * a.tiles_c;
   a.xcds = mc.xcds;
-  // an XCD's tiles in flight, 8 columns wide: 16384x6912x1280 141 us, 16 wide 147, 4 144, 2 150
-  a.band_cols = a.tiles_c < 8 ? a.tiles_c : 8;
+  a.band_cols = mm_band(a.tiles_c);
   a.nk = (int32_t)ceil_div(a.K, C::KS);
   a.tail = (int32_t)((a.K - (int64_t)(a.nk - 1) * C::KS) / 16);
-  int64_t grid = (int64_t)mc.cus * C::PERCU;
-  if (a.tiles < grid) grid = round_up(a.tiles, mc.xcds);
+  const int64_t grid = mm_grid(a.tiles, C::PERCU, mc);
   if (a.o.kind == OUT_BF16)
     hipLaunchKernelGGL((tgemm_int8<C, E, true>), dim3((unsigned)grid), dim3(C::NT), 0, stream, a);
   else
@@ -824,47 +831,63 @@ int launch_mm(MArgs a, const Machine &mc, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
 }
 // The tile with the least estimated time: rounds of tiles over the CUs, each of
-// `step` us a step and at its end of `end` us, `out` for each 2 bytes that it moves
+// `step` us a step and at its end `end` us, `out` for each 2 bytes that it moves
 // an output column of the product, and `act` if it takes a sigmoid of each.  A last
-// round that leaves CUs idle has faster steps; of the two kernels with two
-// workgroups a CU, a last round of one a CU has its own figures.  Fitted to 88 calls
-// of 65 to 16384 rows, with and without Z and an activation, bfloat16 and float32:
-// the choice is the fastest of these six or within 2% of it on 72 of them, and 1.7%
-// slower in the mean.  (Rows of less than half a launch's CUs are best with small
-// tiles: 128x4096x4096 takes 11.3 us in 64x64 and 17.6 in 128x128; large outputs with
-// large ones: 16384x6912x1280 takes 141 us in 256x192, 152 in 256x128, 158 in 128x192.)
+// round that leaves CUs idle has up to 20% faster steps and, since its stores do
+// not meet all the other CUs', down to a quarter of `out`; of the two kernels with two
+// workgroups a CU, a last round of one a CU has its own figures.  Fitted to 578 calls
+// of 65 to 16384 rows, bfloat16 and float32, with and without Z, a residual and a
+// sigmoid: the choice is the fastest of the six or within 2% of it on 516 of them,
+// past 10% on 7 (18% at most, float32 with Z and more than one round), and 0.6% slower
+// in the mean.  (Few tiles are best small: 128x4096x4096 takes 11.4 us in 64x64 and 17.6
+// in 128x128, 200x1280x1280 float32 with residual and Z 7.4 and 12.3; large outputs best
+// large: 16384x6912x1280 takes 141 us in 256x192, 152 in 256x128, 158 in 128x192.)
 struct TileTime {
-  double step, end, out, act, step1, end1;
+  int32_t bm, bn, percu;
+  double step, end, out, act, step1, end1, out1, act1;
 };
-template <class C, int E>
-double time_of(const MArgs &a, const Machine &mc, const TileTime &t) {
-  const int64_t tiles = ceil_div(a.R, C::BM) * ceil_div(a.Cc, C::BN), slots = (int64_t)mc.cus * C::PERCU;
-  const double steps = (double)ceil_div(a.K, C::KS), full = (double)(tiles / slots);
-  const double bytes = (a.o.kind == OUT_BF16 ? 2 : 4) *
-                       (E & EPI_GATED ? 0.5 + (a.o.z ? 1 : 0) : 1.0 + (a.o.z ? 1 : 0) + (a.o.res ? 1 : 0));
-  const double out = bytes / 2, act = (E & kEpiAct) == EPI_SIGM ? (E & EPI_GATED ? 0.5 : 1.0) : 0.0;
-  const int64_t rem = tiles % slots;
-  double us = full * (t.step * steps + t.end + t.out * out + t.act * act);
-  if (rem && C::PERCU == 2 && rem <= mc.cus) {
-    us += t.step1 * steps + t.end1 * (0.5 + 0.5 * out);
-  } else if (rem) {
-    const double fill = (double)rem / (double)slots;
-    us += t.step * (0.75 + 0.25 * fill) * steps + t.end + t.out * out * fill + t.act * act;
+template <class C>
+constexpr TileTime tile_time(double step, double end, double out, double act, double step1 = 0, double end1 = 0,
+                             double out1 = 0, double act1 = 0) {
+  return {C::BM, C::BN, C::PERCU, step, end, out, act, step1, end1, out1, act1};
+}
+constexpr TileTime kTiles[] = {
+    tile_time<T256x192>(1.14, 4.17, 4.44, 0.71),
+    tile_time<T256x128>(0.79, 2.71, 2.95, 0.35),
+    tile_time<T128x192>(0.64, 2.5, 2.12, 0.84),
+    tile_time<T128x128>(0.51, 1.9, 1.4, 0.2),
+    tile_time<T64x128>(0.67, 0.92, 1.51, 0.0, 0.38, 1.38, 0.67, 0.42),
+    tile_time<T64x64>(0.4, 0.8, 0.71, 0.0, 0.26, 1.09, 0.35, 0.13)};
+constexpr int kNumTiles = sizeof(kTiles) / sizeof(kTiles[0]);
+// out: 2-byte units written and read at a tile's end for each column of the product,
+// act: sigmoids for each
+double time_of(const TileTime &t, int64_t R, int64_t Cc, int64_t K, double out, double act, int64_t cus) {
+  const int64_t tiles = ceil_div(R, t.bm) * ceil_div(Cc, t.bn), slots = cus * t.percu, rem = tiles % slots;
+  const double steps = (double)ceil_div(K, kStep), full = (double)(tiles / slots);
+  const double us = full * (t.step * steps + t.end + t.out * out + t.act * act);
+  if (rem == 0) return us;
+  const bool one = t.percu == 2 && rem <= cus;
+  const double fill = (double)rem / (double)(one ? cus : slots), fs = 0.8 + 0.2 * fill, fo = 0.25 + 0.75 * fill;
+  return us + (one ? t.step1 * fs * steps + t.end1 + t.out1 * fo * out + t.act1 * act
+                   : t.step * fs * steps + t.end + t.out * fo * out + t.act * act);
+}
+int best_tile(int64_t R, int64_t Cc, int64_t K, bool gated, int kind, int act, bool z, bool res, int64_t cus) {
+  const double out = (kind == OUT_BF16 ? 1.0 : 2.0) * (gated ? 0.5 + z : 1.0 + z + res);
+  const double sg = epi_of(act) == EPI_SIGM ? (gated ? 0.5 : 1.0) : 0.0;
+  int best = 0;
+  double least = time_of(kTiles[0], R, Cc, K, out, sg, cus);
+  for (int i = 1; i < kNumTiles; ++i) {
+    const double us = time_of(kTiles[i], R, Cc, K, out, sg, cus);
+    if (us < least) {
+      best = i;
+      least = us;
+    }
   }
-  return us;
+  return best;
 }
 template <int E>
 int pick_mm(const MArgs &a, const Machine &mc, hipStream_t stream) {
-  const double us[] = {time_of<T256x192, E>(a, mc, {1.0, 4.0, 4.4, 2.4, 0, 0}),
-                       time_of<T256x128, E>(a, mc, {0.69, 3.1, 2.4, 1.9, 0, 0}),
-                       time_of<T128x192, E>(a, mc, {0.59, 2.2, 1.9, 1.6, 0, 0}),
-                       time_of<T128x128, E>(a, mc, {0.43, 2.0, 1.0, 1.1, 0, 0}),
-                       time_of<T64x128, E>(a, mc, {0.51, 1.9, 1.0, 0.8, 0.32, 1.1}),
-                       time_of<T64x64, E>(a, mc, {0.33, 1.4, 0.4, 0.5, 0.18, 1.6})};
-  int best = 0;
-  for (int i = 1; i < 6; ++i)
-    if (us[i] < us[best]) best = i;
-  switch (best) {
+  switch (best_tile(a.R, a.Cc, a.K, E & EPI_GATED, a.o.kind, a.o.act, a.o.z, a.o.res, mc.cus)) {
     case 0: return launch_mm<T256x192, E>(a, mc, stream);
     case 1: return launch_mm<T256x128, E>(a, mc, stream);
     case 2: return launch_mm<T128x192, E>(a, mc, stream);
@@ -924,13 +947,50 @@ int launch_few(FewArgs a, hipStream_t stream) {
     hipLaunchKernelGGL((int8_few<MF, NB, WAVES, EPI_SIGM | EPI_COLS>), grid, block, 0, stream, a);
   return hipGetLastError() == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
 }
-// column blocks as wide as leaves every CU one, and sixteen waves where a block
-// of 16 has more super-steps than eight
+// 16 or 32 rows, column blocks as wide as leaves every CU one, and sixteen waves where a
+// block of 16 has more super-steps than eight
+struct FewPlan {
+  int32_t mf, nb, waves;
+};
+FewPlan few_plan(int64_t M, int64_t N, int64_t K, int64_t cus) {
+  const int32_t nb = N >= 64 * cus ? 4 : N >= 32 * cus ? 2 : 1;
+  return {M <= 16 ? 1 : 2, nb, nb == 1 && K > 8 * kFewStep ? 16 : 8};
+}
 template <int MF>
-int pick_few(const FewArgs &a, int64_t cus, hipStream_t stream) {
-  if (a.N >= 64 * cus) return launch_few<MF, 4, 8>(a, stream);
-  if (a.N >= 32 * cus) return launch_few<MF, 2, 8>(a, stream);
-  return a.K > 8 * kFewStep ? launch_few<MF, 1, 16>(a, stream) : launch_few<MF, 1, 8>(a, stream);
+int pick_few(const FewArgs &a, const FewPlan &p, hipStream_t stream) {
+  if (p.nb == 4) return launch_few<MF, 4, 8>(a, stream);
+  if (p.nb == 2) return launch_few<MF, 2, 8>(a, stream);
+  return p.waves == 16 ? launch_few<MF, 1, 16>(a, stream) : launch_few<MF, 1, 8>(a, stream);
+}
+
+// The plans' common part, and those of tgemm_int8
+int start_plan(int64_t M, int64_t Cc, int64_t K, int act, int out_kind, int32_t cus, int32_t xcds, tgemm_plan *plan) {
+  if (cus < 1 || xcds < 1 || cus % xcds != 0) return TGEMM_ERR_DIM;
+  if (out_kind != TGEMM_OUT_F32 && out_kind != TGEMM_OUT_BF16) return TGEMM_ERR_KIND;
+  if (act < TGEMM_ACT_NONE || act > TGEMM_ACT_GELU_TANH) return TGEMM_ERR_VALUE;
+  *plan = {};
+  plan->out_rows = M;
+  plan->out_cols = Cc;
+  plan->contraction = K;
+  plan->xcds = xcds;
+  return TGEMM_OK;
+}
+void tile_plan(int tile, int64_t R, int64_t Cc, const Machine &mc, tgemm_plan *plan) {
+  static constexpr int kThreads[] = {T256x192::NT, T256x128::NT, T128x192::NT, T128x128::NT, T64x128::NT, T64x64::NT};
+  static constexpr int kBytes[] = {T256x192::kLds + T256x192::kAuxBytes, T256x128::kLds + T256x128::kAuxBytes,
+                                   T128x192::kLds + T128x192::kAuxBytes, T128x128::kLds + T128x128::kAuxBytes,
+                                   T64x128::kLds + T64x128::kAuxBytes,   T64x64::kLds + T64x64::kAuxBytes};
+  static_assert(sizeof(kThreads) / sizeof(int) == kNumTiles && sizeof(kBytes) / sizeof(int) == kNumTiles, "tiles");
+  const TileTime &t = kTiles[tile];
+  plan->kernel = TGEMM_KERNEL_INT8;
+  plan->tile_rows = t.bm;
+  plan->tile_cols = t.bn;
+  plan->tiles = ceil_div(R, t.bm) * ceil_div(Cc, t.bn);
+  plan->workgroups = mm_grid(plan->tiles, t.percu, mc);
+  plan->tiles_per_workgroup = ceil_div(ceil_div(plan->tiles, mc.xcds), plan->workgroups / mc.xcds);
+  plan->band_cols = mm_band((int32_t)ceil_div(Cc, t.bn));
+  plan->threads_per_workgroup = kThreads[tile];
+  plan->lds_bytes = kBytes[tile];
 }
 
 }  // namespace
@@ -979,13 +1039,60 @@ int ternary_gemm_s8s8_epilogue(const int8_t *A, const int8_t *W, const float *a_
   const bool copy = K % 16 != 0 || align_of(A) % 16 != 0 || align_of(W) % 16 != 0;
   if (few_rows(M, N, K, copy)) {
     const FewArgs a = {A, W, o, M, N, K, 0, mc.xcds};
-    return M <= 16 ? pick_few<1>(a, mc.cus, stream) : pick_few<2>(a, mc.cus, stream);
+    const FewPlan p = few_plan(M, N, K, mc.cus);
+    return p.mf == 1 ? pick_few<1>(a, p, stream) : pick_few<2>(a, p, stream);
   }
   int8_t *la = static_cast<int8_t *>(workspace), *lw = la + l.a_bytes;
   if (l.a_bytes) lay(A, la, M, K, l.kp, stream);
   if (l.w_bytes) lay(W, lw, N, K, l.kp, stream);
   const MArgs a = {l.a_bytes ? la : A, l.w_bytes ? lw : W, o, M, N, l.kp, 0, 0, 0, 0, 0, 0, 0};
   return pick_mm_act<EPI_COLS>(a, mc, stream);
+}
+
+int ternary_gemm_s8s8_plan(int64_t M, int64_t N, int64_t K, int64_t align, int act, int residual, int save, int out_kind,
+                           int32_t cus, int32_t xcds, tgemm_plan *plan) {
+  if (!plan) return TGEMM_ERR_NULL;
+  int st = check_sizes(M, N, K);
+  if (st != TGEMM_OK) return st;
+  if (K > TGEMM_INT8_MAX_CONTRACTION) return TGEMM_ERR_BOUND;
+  st = start_plan(M, N, K, act, out_kind, cus, xcds, plan);
+  if (st != TGEMM_OK) return st;
+  const bool copy = K % 16 != 0 || align < 1 || align % 16 != 0;
+  plan->fast_path = copy ? 0 : 1;
+  if (few_rows(M, N, K, copy)) {
+    const FewPlan p = few_plan(M, N, K, cus);
+    plan->kernel = TGEMM_KERNEL_INT8_FEW;
+    plan->tile_rows = 16 * p.mf;
+    plan->tile_cols = 16 * p.nb;
+    plan->band_cols = (int32_t)ceil_div(N, 16 * p.nb);
+    plan->tiles = plan->workgroups = plan->band_cols * ceil_div(M, 16 * p.mf);
+    plan->tiles_per_workgroup = 1;
+    plan->threads_per_workgroup = 64 * p.waves;
+    plan->lds_bytes = 16 * p.waves * 16 * p.mf * (4 * p.nb + 1);
+  } else {
+    tile_plan(best_tile(M, N, round_up(K, 16), false, out_kind, act, save != 0, residual != 0, cus), M, N, {cus, xcds}, plan);
+  }
+  return TGEMM_OK;
+}
+
+int ternary_gemm_s8_gated_plan(int64_t M, int64_t N, int64_t K, int64_t align, int act, int save, int out_kind, int32_t cus,
+                               int32_t xcds, tgemm_plan *plan) {
+  if (!plan) return TGEMM_ERR_NULL;
+  int st = check_sizes(M, N, K);
+  if (st != TGEMM_OK) return st;
+  if (K % 4 != 0) return TGEMM_ERR_PACK;
+  if (K > TGEMM_TERNARY_MAX_CONTRACTION) return TGEMM_ERR_BOUND;
+  st = start_plan(M, 2 * N, K, act, out_kind, cus, xcds, plan);
+  if (st != TGEMM_OK) return st;
+  if (align < 1) align = 1;
+  if (gated_few_ok(M, N, K, align)) {
+    plan->fast_path = 1;
+    gated_few_plan(M, N, K, cus, xcds, plan);
+  } else {
+    plan->fast_path = K % 16 == 0 && align % 16 == 0;
+    tile_plan(best_tile(M, 2 * N, round_up(K, 16), true, out_kind, act, save != 0, false, cus), M, 2 * N, {cus, xcds}, plan);
+  }
+  return TGEMM_OK;
 }
 
 int ternary_gemm_s8_gated_workspace(int64_t M, int64_t N, int64_t K, int64_t align, int64_t *bytes) {

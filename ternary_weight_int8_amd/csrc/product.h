@@ -470,8 +470,8 @@ __device__ __forceinline__ v4i decode16(uint32_t x) {
 }  // namespace
 
 // The gated product of few rows on the stored codes, in ternary_gemm.hip: whether
-// it takes these sizes and this smallest alignment of A and Wpacked, and the call
-// (arguments checked by the caller).
+// it takes these sizes and this smallest alignment of A and Wpacked, its launch, and
+// the call (arguments checked by the caller).
 struct GatedCall {
   const int8_t *A;
   const uint8_t *Wpacked;
@@ -482,6 +482,8 @@ struct GatedCall {
   int64_t M, N, K;
 };
 __attribute__((visibility("hidden"))) bool gated_few_ok(int64_t M, int64_t N, int64_t K, int64_t align);
+__attribute__((visibility("hidden"))) void gated_few_plan(int64_t M, int64_t N, int64_t K, int32_t cus, int32_t xcds,
+                                                          tgemm_plan *plan);
 __attribute__((visibility("hidden"))) int gated_few(const GatedCall &c, int32_t cus, int32_t xcds, hipStream_t stream);
 
 #endif  // TERNARY_PRODUCT_H

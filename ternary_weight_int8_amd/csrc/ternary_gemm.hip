@@ -2825,6 +2825,18 @@ bool gated_few_ok(int64_t M, int64_t N, int64_t K, int64_t align) {
   return (M <= 128 || (M <= 192 && N <= 8192)) && K % 64 == 0 && align % 16 == 0 && N <= (INT32_MAX - 64) / 2 && K <= INT32_MAX;
 }
 
+void gated_few_plan(int64_t M, int64_t N, int64_t K, int32_t cus, int32_t xcds, tgemm_plan *plan) {
+  const SkinnyPlan kp = skinny_plan(FWD, M < 32 ? M : 32, 2 * N, K, 16, 16, {cus, xcds});
+  plan->kernel = KSKINNY;
+  plan->tile_rows = 16 * kp.mf;
+  plan->tile_cols = 16 * kp.nb;
+  plan->tiles = plan->workgroups = kp.grid * ceil_div(M, 32);
+  plan->tiles_per_workgroup = 1;
+  plan->band_cols = kp.grid;
+  plan->threads_per_workgroup = sk::kNT;
+  plan->lds_bytes = kp.lds;
+}
+
 int gated_few(const GatedCall &c, int32_t cus, int32_t xcds, hipStream_t stream) {
   const SkinnyPlan kp = skinny_plan(FWD, c.M < 32 ? c.M : 32, 2 * c.N, c.K, 16, 16, {cus, xcds});
   KArgs ka{};
@@ -3025,10 +3037,24 @@ int ternary_gemm_tile_of(const tgemm_plan *plan, int64_t workgroup, int64_t iter
     tr = (int32_t)((start + pos) / tiles_c);
     tc = (int32_t)((start + pos) % tiles_c);
   } else if (plan->kernel == KSKINNY) {
-    // all rows; the column block in the XCD-contiguous order
+    // all rows, or (gated) a block of them after another; the column block in the XCD-contiguous order
     if (iteration != 0) return TGEMM_ERR_DIM;
-    tr = 0;
-    tc = xcd_tile((int32_t)workgroup, tiles, xcds);
+    tr = (int32_t)workgroup / tiles_c;
+    tc = xcd_tile((int32_t)workgroup % tiles_c, tiles_c, xcds);
+  } else if (plan->kernel == TGEMM_KERNEL_INT8) {
+    // as the stream kernel's, in bands
+    if (plan->workgroups % xcds != 0) return TGEMM_ERR_DIM;
+    const int32_t nx = (int32_t)plan->workgroups / xcds, xcd = (int32_t)(workgroup % xcds);
+    const int32_t qx = tiles / xcds, rx = tiles % xcds;
+    const int64_t pos = workgroup / xcds + iteration * nx;
+    if (pos >= qx + (xcd < rx ? 1 : 0)) return TGEMM_ERR_DIM;
+    tile_rc(xcd * qx + (xcd < rx ? xcd : rx) + (int32_t)pos, tiles / tiles_c, tiles_c, plan->band_cols, &tr, &tc);
+  } else if (plan->kernel == TGEMM_KERNEL_INT8_FEW) {
+    // the row blocks of a column block together
+    if (iteration != 0) return TGEMM_ERR_DIM;
+    const int32_t pos = xcd_tile((int32_t)workgroup, tiles, xcds), rblocks = tiles / tiles_c;
+    tr = pos % rblocks;
+    tc = pos / rblocks;
   } else {
     if (iteration != 0) return TGEMM_ERR_DIM;
     tile_rc(xcd_tile((int32_t)workgroup, tiles, xcds), tiles / tiles_c, tiles_c, plan->band_cols, &tr, &tc);
