@@ -91,3 +91,45 @@ def test_every_output_tile_covered_once(op, M, N, K, cus, xcds):
     assert pl.out_cols == (N if op == "s8s8" else 2 * N)
     assert len(seen) == len(want) == pl.tiles and set(seen) == want
     assert pl.lds_bytes <= 160 * 1024 and pl.threads_per_workgroup in (256, 512, 1024)
+
+
+STAGES = {(256, 192): 2, (256, 128): 3, (128, 192): 3, (128, 128): 4, (64, 128): 3, (64, 64): 4}
+
+
+def plans_of(op, M, N, K):
+    """(plan, kind, sigmoid, save, residual) of the calls that the GPU tests make at a size."""
+    for kind in KIND.values():
+        for act in ("relu", "silu"):
+            for save in (False, True):
+                for res in (False, True) if op == "s8s8" else (False,):
+                    pl = (B.s8s8_plan(M, N, K, act=act, residual=res, save=save, kind=kind) if op == "s8s8" else
+                          B.gated_plan(M, N, K, act=act, save=save, kind=kind))
+                    yield pl, kind, act == "silu", save, res
+
+
+@pytest.mark.parametrize("op", ["s8s8", "gated"])
+def test_gpu_tests_reach_every_kernel(op):
+    """Each of the six tiles in each form, with more than one tile a workgroup, tiles inside the output and past its
+    last row and column, a last step that is not whole, steps up to a tile's stages and more; every few-row kernel."""
+    pytest.importorskip("torch")
+    import test_gpu_int8_kernels as gpu
+    tiles, deep, few = set(), set(), set()
+    for M, N, K in (gpu.INT8_TILES + gpu.INT8_FEW if op == "s8s8" else gpu.GATED_TILES + gpu.GATED_FEW):
+        for pl, *form in plans_of(op, M, N, K):
+            t = tile(pl)
+            if pl.kernel != B.KERNEL_INT8:
+                few.add((*t, pl.threads_per_workgroup, M > 8 if op == "gated" else None, form[1]))
+                continue
+            whole = M // t[0] >= 2 and pl.out_cols // t[1] >= 2
+            if whole and pl.tiles_per_workgroup >= 2 and M % t[0] and pl.out_cols % t[1] and K % 128:
+                tiles.add((*t, *form))
+                deep.add((*t, form[0], -(-K // 128) > STAGES[t]))
+    assert tiles == {(*t, k, s, z, r) for t in TILES for k in KIND.values() for s in (False, True) for z in (False, True)
+                     for r in ((False, True) if op == "s8s8" else (False,))}
+    assert {(*t, k, True) for t in TILES for k in KIND.values()} <= deep
+    if op == "s8s8":
+        want = {(r, c, w) for r in (16, 32) for c, w in ((16, 512), (16, 1024), (32, 512), (64, 512))}
+        assert few == {(*x, None, s) for x in want for s in (False, True)}
+    else:
+        want = {(16, c, al) for c in (16, 32, 64) for al in (False, True)} | {(32, c, True) for c in (16, 32, 64)}
+        assert few == {(r, c, 512, al, s) for r, c, al in want for s in (False, True)}
