@@ -947,9 +947,10 @@ __global__ __launch_bounds__(max_t(W, V)) void ln_reg(LnArgs a) {
       if (a.beta) load_f<U>(a.beta + un.off[j], beta[j]);
     }
   }
-  // kSplit: the lane's elements (0 in lanes past the row), one over lane 0's, and the wave's
-  const float own = (float)(U * un.n - (un.last >= 0 ? un.dup : 0)), per = __fdiv_rn(1.f, fmaxf(own, 1.f));
-  const double wave_own = (double)wave_sum(own);
+  // kSplit: the lane's elements (0 in lanes past the row), about one over them (lane 0's
+  // serves), and the wave's
+  const float own = (float)(U * un.n - (un.last >= 0 ? un.dup : 0)), per = __builtin_amdgcn_rcpf(fmaxf(own, 1.f));
+  const double wave_own = W ? a.n : (double)wave_sum(own);
   int flip = 0;
   const int groups = W ? (int)(blockDim.x >> 6) : 1;
   const int64_t stride = (int64_t)gridDim.x * groups;
