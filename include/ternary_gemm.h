@@ -370,7 +370,8 @@ int ternary_epilogue_backward_workspace(int64_t R, int64_t C, int64_t *bytes);
  *   beta        float [C], or NULL for 0
  *   mean, rstd  float [R] each, or both NULL (the backward pass takes them)
  * In float32 the mean that y and rstd are taken with is held to more than 32 bits;
- * mean[r] is its nearest float.
+ * mean[r] is its nearest float, and the backward pass takes it as given: its xhat is
+ * off by up to half a step of mean[r] times rstd[r].
  */
 int ternary_layernorm_quantize(const void *X, int in_kind, const void *residual, const float *gain, const float *beta,
                                float eps, void *H, void *Y, float *mean, float *rstd, int8_t *Q, float *scale,

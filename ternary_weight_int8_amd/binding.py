@@ -4,7 +4,8 @@ Every product runs in the library's HIP kernels.  There is no fallback: if the
 library is missing or a call fails, these functions raise.  PyTorch supplies
 device memory and the current stream; the library never allocates.  A call
 launches on the current HIP device, which has to be its tensors' (one process a
-GPU).
+GPU); the layer norm, the gated layer and the product with int8 weights refuse
+tensors of another, the other calls leave that to the caller.
 """
 from __future__ import annotations
 

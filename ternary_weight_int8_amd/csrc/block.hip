@@ -841,7 +841,9 @@ __global__ __launch_bounds__(kNT) void col_sums(const T *__restrict__ A, const T
 // Bound by HBM: 16384x1280
 // bf16 with residual and Y, 189 MB, 34 us (the RMS norm 33), 16384x3456 float32, 963 MB,
 // 188 us.  Column sums of both kinds (dgain, dbeta) cost the backward pass little more
-// than one: 16384x3456 bf16 91 us against 84, 16384x1280 float32 62 against 60.
+// than one: 16384x3456 bf16 91 us against 84, 16384x1280 float32 62 against 60.  Its float32
+// rows past 12288 spill 87 registers: 2048x14336 174 us (a copy's rate: 89), where
+// 2048x11008, without, takes 86 (68).
 // ---------------------------------------------------------------------------
 struct LnArgs {
   const void *X, *res;
@@ -1262,6 +1264,11 @@ __global__ __launch_bounds__(kNT) void ln_bwd_rows(LnBwdArgs a) {
 // product with both matrices' codes adds the two parts of dX up.  One pass over dY and
 // Z, the row's 2 C values kept in registers between its largest magnitude and its int8
 // row: 16384x3456 bf16, 680 MB, takes 144 us with silu (4.7 TB/s) and 4.7 for col_finish.
+// Past 8192 columns a workgroup's sixteen waves hold two bfloat16 units a lane, or three
+// or four float32 ones, in 128 registers, and spill: two 21 to 23 of them, three 21 to
+// 26, four 64 to 70.  silu, column sums and all: 4096x11008 bf16 163 us (a copy's rate:
+// 102), 4096x14336 193 (133), 4096x16384 209 (152); 2048x11008 float32 128 (94), 2048x14336
+// 220 (122).
 // ---------------------------------------------------------------------------
 struct GatedBwdArgs {
   const void *dY, *Z;
@@ -1732,8 +1739,10 @@ RowPlan row_plan(int64_t R, int64_t C, int kind, bool sums, bool one_ok = true) 
 // of 16): 16384x3456 70 -> 50 us (with residual and Y 115 -> 98), 8000x7000 84 ->
 // 53, 8000x5000 (five waves) equal, 6000x6000 (six) 45 -> 49 and left. float32:
 // three units, but two where those are four, seven or eight waves and three would
-// be three, five or six: 16384x1280 52 -> 29 us at three and 32 at two, 8000x2000
-// 34 -> 21 and 19, 10000x2600 65 -> 31 and 47, 16384x3456 129 -> 87 and 76.
+// be three, five or six.  At one, two and three units: 16384x1280 58, 33 and 29 us, 8000x2000
+// 38, 21 and 23, 16384x3456 168, 79 and 93; at two and three past 4096: 8000x5000 79 and
+// 50, 6000x7000 68 and 66, 6000x8192 70 and 73, and with a residual alike (8000x5000 106 and
+// 101) but for 8000x4100, 81 and 87.
 RowPlan ln_plan(int64_t R, int64_t C, int kind) {
   RowPlan p = row_plan(R, C, kind, false);
   const bool f32 = kind == TGEMM_IN_F32;
@@ -1804,7 +1813,9 @@ void row_launch(int kind, const RowPlan &p, const typename Kernel::Args &a, hipS
 
 // The passes with two column sums: their plan is row_plan's but for few rows, which
 // one workgroup takes (write_cols_one), up to three units a lane in float32 and two
-// in bfloat16 (three spill).  That saves the second launch and the workspace: the
+// in bfloat16.  (Its sixteen waves leave a lane 128 registers: at these largest widths the
+// gated pass spills 19 to 24 of them, and the norm's bfloat16 one 2.)  That saves the
+// second launch and the workspace: the
 // norm, 27x729 f32, 11.4 against 15.9 us a call (8.3 against 5.6 in a graph), 27x243
 // 11.4 and 16.0 (4.5 and 6.4), 32x1000 bf16 13.5 and 16.1 (10.9 and 6.1).  The gated
 // pass has several times the instructions, and one CU for all of them: past two units
